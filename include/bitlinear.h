@@ -351,6 +351,123 @@ BITLINEAR_API bitlinear_status bitlinear_gemv_tl2_grouped(const bitlinear_tl2_pr
                                                           int64_t count, int64_t N,
                                                           bitlinear_stream_t stream);
 
+/* ------------------------------------------------- between two products */
+
+/*
+ * What a decoder layer does between two ternary products, in one launch each:
+ * residual addition and norm, or gate and norm, in front of the quantiser;
+ * bias, activation and residual behind the product.  Activation matrices may
+ * be fp32, bf16 or fp16 here, with a row stride of their own (in elements), so
+ * that they can be views of wider buffers.  All arithmetic is fp32 unless a
+ * line says 64 bits; each operation is rounded once.
+ */
+typedef enum {
+    BITLINEAR_F32 = 0,
+    BITLINEAR_BF16 = 1,
+    BITLINEAR_F16 = 2
+} bitlinear_dtype;
+
+typedef enum {
+    BITLINEAR_ACT_NONE = 0,
+    BITLINEAR_ACT_RELU = 1,       /* max(v, 0) */
+    BITLINEAR_ACT_RELU2 = 2,      /* max(v, 0)^2 */
+    BITLINEAR_ACT_SILU = 3,       /* v / (1 + e^-v) */
+    BITLINEAR_ACT_GELU = 4,       /* v/2 (1 + erf(v / sqrt 2)) */
+    BITLINEAR_ACT_GELU_TANH = 5   /* v/2 (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) */
+} bitlinear_act_kind;
+
+/* One norm + quantise call. */
+typedef struct {
+    const void* x;            /* [N, K] of dtype, row stride ldx */
+    const void* residual;     /* [N, K] of dtype, row stride ldr, or NULL */
+    void* h;                  /* [N, K] of dtype, row stride ldh: output; NULL iff residual is */
+    const float* weight;      /* [K] fp32 norm weight, or NULL (all ones) */
+    int8_t* xq;               /* [N, K] output, contiguous */
+    float* amax;              /* [N] output */
+    int32_t* xsum;            /* [N] output, or NULL */
+    int64_t N, K;
+    int64_t ldx, ldr, ldh;
+    double eps;
+    int dtype;                /* bitlinear_dtype of x, residual and h */
+    int normalize;            /* 0: no norm, the rows of h are quantised as they are */
+} bitlinear_norm;
+
+/*
+ * Root-mean-square norm with the residual's addition, and int8 output with one
+ * scale per token (the quantiser of bitlinear_quant_act behind it):
+ *   h    = x, or with a residual x + residual rounded to dtype (written out)
+ *   r    = 1 / sqrt(sum_k h^2 / K + eps)     in 64 bits, rounded once to fp32
+ *   v    = (h * r) * weight                   (v = h when normalize is 0)
+ *   amax = max_k |v|;  xq, xsum as in bitlinear_quant_act
+ * eps must be positive and finite, and weight NULL without the norm.  A row
+ * whose v holds NaN or inf gets amax = NaN, xq = 0 and xsum = 0, so that its
+ * products come out NaN; other rows are not affected.
+ * h may be x or residual itself (same pointer and stride); any other overlap
+ * of an output with another operand is an error of the caller.
+ * x, residual and h: 16-byte aligned, row strides (when N > 1) at least K and
+ * multiples of 16 bytes.  weight 16-byte aligned.  One launch, no workspace.
+ */
+BITLINEAR_API bitlinear_status bitlinear_norm_quant(const bitlinear_norm* a,
+                                                    bitlinear_stream_t stream);
+
+/* One gate + norm + quantise call. */
+typedef struct {
+    const void* gate;         /* [N, K] of dtype, row stride ldg */
+    const void* up;           /* [N, K] of dtype, row stride ldu */
+    const float* weight;      /* [K] fp32 norm weight, or NULL (all ones) */
+    int8_t* xq;               /* [N, K] output, contiguous */
+    float* amax;              /* [N] output */
+    int32_t* xsum;            /* [N] output, or NULL */
+    int64_t N, K;
+    int64_t ldg, ldu;
+    double eps;
+    int dtype;                /* bitlinear_dtype of gate and up */
+    int activation;           /* bitlinear_act_kind */
+    int normalize;            /* 0: no norm */
+} bitlinear_gated_norm;
+
+/*
+ * The middle of a gated MLP, the input of its down projection:
+ * h = act(gate) * up in fp32 (not rounded to dtype), then as in
+ * bitlinear_norm_quant.  The rules on eps, weight, alignment and non-finite
+ * rows are the same.
+ */
+BITLINEAR_API bitlinear_status bitlinear_gated_norm_quant(const bitlinear_gated_norm* a,
+                                                          bitlinear_stream_t stream);
+
+/* One layer of a bitlinear_linear call. */
+typedef struct {
+    const uint32_t* packed;   /* [M, WP(K)] words */
+    const float* alpha;       /* [1] */
+    int64_t M;
+    int64_t K;
+    const int8_t* xq;         /* [N, K] */
+    const float* amax;        /* [N] */
+    const int32_t* xsum;      /* [N] */
+    const float* bias;        /* [M] fp32, or NULL */
+    const void* residual;     /* [N, M] of dtype, row stride ldr, or NULL */
+    void* y;                  /* [N, M] of dtype, row stride ldy: output */
+    int64_t ldr, ldy;
+    int dtype;                /* bitlinear_dtype of residual and y */
+    int activation;           /* bitlinear_act_kind */
+} bitlinear_linear_problem;
+
+/*
+ * The ternary product with its epilogue, over a list of layers that share the
+ * token count (as bitlinear_gemm_grouped does):
+ *   y[n,m] = act(acc[n,m] * (alpha * (amax[n]/127)) + bias[m]) + residual[n,m]
+ * in fp32, rounded once to dtype.  Any N: one token runs on the CUDA cores,
+ * more on the tensor cores.  y may be the residual itself (same pointer and
+ * stride); any other overlap is an error of the caller.
+ * bias 4-byte aligned; residual and y aligned to an element, row strides (when
+ * N > 1) at least M; the other pointers as in bitlinear_gemm.  `problems` is a
+ * HOST array read during the call only; all layers are checked before
+ * anything is launched.
+ */
+BITLINEAR_API bitlinear_status bitlinear_linear(const bitlinear_linear_problem* problems,
+                                                int64_t count, int64_t N,
+                                                bitlinear_stream_t stream);
+
 /* ------------------------------------------------- weights, no allocation */
 
 /*

@@ -21,6 +21,10 @@ ERR_CUDA = 5
 ERR_DEVICE_TIMEOUT = 6
 ERR_NONFINITE = 7
 
+# bitlinear_dtype and bitlinear_act_kind
+F32, BF16, F16 = 0, 1, 2
+ACT_NONE, ACT_RELU, ACT_RELU2, ACT_SILU, ACT_GELU, ACT_GELU_TANH = range(6)
+
 
 class Problem(ctypes.Structure):
     """Mirror of bitlinear_problem (include/bitlinear.h)."""
@@ -47,6 +51,33 @@ class Tl2Problem(ctypes.Structure):
     _fields_ = [("tl2", ctypes.c_void_p), ("alpha", ctypes.c_void_p), ("M", ctypes.c_int64),
                 ("K", ctypes.c_int64), ("xq", ctypes.c_void_p), ("amax", ctypes.c_void_p),
                 ("y", ctypes.c_void_p), ("acc", ctypes.c_void_p)]
+
+
+class Norm(ctypes.Structure):
+    """Mirror of bitlinear_norm (include/bitlinear.h)."""
+    _fields_ = [("x", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("h", ctypes.c_void_p),
+                ("weight", ctypes.c_void_p), ("xq", ctypes.c_void_p), ("amax", ctypes.c_void_p),
+                ("xsum", ctypes.c_void_p), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("ldx", ctypes.c_int64), ("ldr", ctypes.c_int64), ("ldh", ctypes.c_int64),
+                ("eps", ctypes.c_double), ("dtype", ctypes.c_int), ("normalize", ctypes.c_int)]
+
+
+class GatedNorm(ctypes.Structure):
+    """Mirror of bitlinear_gated_norm (include/bitlinear.h)."""
+    _fields_ = [("gate", ctypes.c_void_p), ("up", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("xq", ctypes.c_void_p), ("amax", ctypes.c_void_p), ("xsum", ctypes.c_void_p),
+                ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("ldg", ctypes.c_int64),
+                ("ldu", ctypes.c_int64), ("eps", ctypes.c_double), ("dtype", ctypes.c_int),
+                ("activation", ctypes.c_int), ("normalize", ctypes.c_int)]
+
+
+class LinearProblem(ctypes.Structure):
+    """Mirror of bitlinear_linear_problem (include/bitlinear.h)."""
+    _fields_ = [("packed", ctypes.c_void_p), ("alpha", ctypes.c_void_p), ("M", ctypes.c_int64),
+                ("K", ctypes.c_int64), ("xq", ctypes.c_void_p), ("amax", ctypes.c_void_p),
+                ("xsum", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("residual", ctypes.c_void_p), ("y", ctypes.c_void_p), ("ldr", ctypes.c_int64),
+                ("ldy", ctypes.c_int64), ("dtype", ctypes.c_int), ("activation", ctypes.c_int)]
 
 
 class BitLinearError(RuntimeError):
@@ -106,6 +137,12 @@ def load(path: str = LIB_PATH):
     L.bitlinear_gemv_tl2.restype = st
     L.bitlinear_gemv_tl2_grouped.argtypes = [ctypes.POINTER(Tl2Problem), i64, i64, p]
     L.bitlinear_gemv_tl2_grouped.restype = st
+    L.bitlinear_norm_quant.argtypes = [ctypes.POINTER(Norm), p]
+    L.bitlinear_norm_quant.restype = st
+    L.bitlinear_gated_norm_quant.argtypes = [ctypes.POINTER(GatedNorm), p]
+    L.bitlinear_gated_norm_quant.restype = st
+    L.bitlinear_linear.argtypes = [ctypes.POINTER(LinearProblem), i64, i64, p]
+    L.bitlinear_linear.restype = st
     L.bitlinear_device_error.argtypes = [ctypes.POINTER(ctypes.c_int), ctypes.c_int]
     L.bitlinear_device_error.restype = st
     L.bitlinear_set_wait_limit.argtypes = [ctypes.c_ulonglong]
@@ -259,6 +296,21 @@ def make_tl2_problems(entries):
 def bitlinear_gemv_tl2_grouped(problems, count, N, stream=None):
     """problems: a ctypes array from make_tl2_problems()."""
     return load().bitlinear_gemv_tl2_grouped(problems, count, N, _stream(stream))
+
+
+def bitlinear_norm_quant(a, stream=None):
+    """a: a Norm."""
+    return load().bitlinear_norm_quant(a, _stream(stream))
+
+
+def bitlinear_gated_norm_quant(a, stream=None):
+    """a: a GatedNorm."""
+    return load().bitlinear_gated_norm_quant(a, _stream(stream))
+
+
+def bitlinear_linear(problems, count, N, stream=None):
+    """problems: a ctypes array of LinearProblem."""
+    return load().bitlinear_linear(problems, count, N, _stream(stream))
 
 
 def bitlinear_pack_workspace_bytes(M, K):

@@ -5,6 +5,8 @@ torch (device memory is torch's job here), and hands raw pointers to one C
 entry point of libbitlinear.so.  All arithmetic runs in the CUDA kernels;
 nothing here falls back to the CPU.
 """
+import contextlib
+
 import torch
 
 from . import _lib
@@ -334,21 +336,265 @@ def gemv_tl2(tl2, alpha, xq, amax, M=None, with_acc=False, stream=None, out=None
     return (y, acc) if with_acc else y
 
 
-class TernaryLinear:
-    """A BitLinear layer: packed 2-bit ternary weights + alpha, applied to fp32
-    activations: the fused quantise+GEMV kernel below GEMM_MIN_TOKENS tokens,
-    else quant_act -> tensor-core GEMM with the fused rescale."""
+# ------------------------------------------------ between two products
 
-    def __init__(self, packed, alpha, in_features, out_features):
-        self.packed, self.alpha = packed, alpha
+# Element types of activation matrices in norm_quant, gated_norm_quant and linear.
+ACT_DTYPES = {torch.float32: _lib.F32, torch.bfloat16: _lib.BF16, torch.float16: _lib.F16}
+
+ACTIVATIONS = {None: _lib.ACT_NONE, "none": _lib.ACT_NONE, "relu": _lib.ACT_RELU,
+               "relu2": _lib.ACT_RELU2, "silu": _lib.ACT_SILU, "gelu": _lib.ACT_GELU,
+               "gelu_tanh": _lib.ACT_GELU_TANH}
+
+
+def _activation(name):
+    try:
+        return ACTIVATIONS[name]
+    except (KeyError, TypeError):
+        raise ValueError("activation must be one of %s, got %r"
+                         % (sorted(k for k in ACTIVATIONS if k), name)) from None
+
+
+def _need_rows(t, name, shape=None, dtype=None):
+    """An activation matrix [N, K] of a known type whose rows are dense (the
+    row stride is free).  Returns its row stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor (no CPU path exists)" % name)
+    if t.dtype not in ACT_DTYPES or (dtype is not None and t.dtype != dtype):
+        raise TypeError("%s must be %s, got %s"
+                        % (name, dtype or "float32, bfloat16 or float16", t.dtype))
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError("%s must have shape %s, got %s"
+                         % (name, shape or "[N, K]", tuple(t.shape)))
+    N, K = t.shape
+    if K > 1 and t.stride(1) != 1:
+        raise ValueError("%s must have dense rows (stride 1 along the last dimension)" % name)
+    ld = t.stride(0) if N > 1 else K
+    if ld < K:
+        raise ValueError("%s: its rows overlap" % name)
+    return ld
+
+
+def _need_vector(t, n, name, device):
+    """An optional fp32 vector of n entries on `device`."""
+    if t is None:
+        return None
+    _need(t, torch.float32, name)
+    if t.numel() != n:
+        raise ValueError("%s must hold %d entries, got %d" % (name, n, t.numel()))
+    _on(device, **{name: t})
+    return t.data_ptr()
+
+
+def _launch(dev, stream, call):
+    """call(raw stream) with `dev` current; raises on a status other than OK."""
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return call(_lib._stream(stream))
+    return call(_lib._stream(stream))
+
+
+def _out_stream(stream, dev):
+    """The context in which a call allocates what it returns: the stream that
+    writes it, so that the memory is not handed out again before that."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    return torch.cuda.stream(stream)
+
+
+def _codes_out(N, K, dev):
+    return (torch.empty((N, K), dtype=torch.int8, device=dev),
+            torch.empty(N, dtype=torch.float32, device=dev),
+            torch.empty(N, dtype=torch.int32, device=dev))
+
+
+def norm_quant(x, weight=None, eps=1e-5, residual=None, normalize=True, h_out=None, stream=None):
+    """Root-mean-square norm, with the residual's addition in front of it, and
+    the per-token int8 quantiser behind it, in one launch.
+
+    x: [N, K] fp32, bf16 or fp16 with dense rows of any row stride (16-byte
+    aligned); residual: another of its type and shape, or None; weight: fp32
+    [K] or None.  Without `normalize` the rows are quantised as they are.
+    Returns (xq, amax, xsum) as quant_act does, or with a residual (h, xq,
+    amax, xsum) with h = x + residual in x's type, which the norm is taken of;
+    h_out may be x or residual, to write it in place.  A row with NaN or inf
+    gets amax NaN and codes 0.  Outputs belong to the stream that writes them.
+    """
+    ldx = _need_rows(x, "x")
+    N, K = x.shape
+    dev = x.device
+    ldr = ldh = 0
+    if residual is not None:
+        ldr = _need_rows(residual, "residual", (N, K), x.dtype)
+        _on(dev, residual=residual)
+        if h_out is not None:
+            _need_rows(h_out, "h_out", (N, K), x.dtype)
+            _on(dev, h_out=h_out)
+    elif h_out is not None:
+        raise ValueError("h_out without a residual: x itself is what the norm is taken of")
+    w = _need_vector(weight, K, "weight", dev)
+    if weight is not None and not normalize:
+        raise ValueError("weight belongs to the norm: pass None without it")
+    with _out_stream(stream, dev):
+        xq, amax, xsum = _codes_out(N, K, dev)
+        h = h_out
+        if residual is not None and h is None:
+            h = torch.empty((N, K), dtype=x.dtype, device=dev)
+    if h is not None:
+        ldh = h.stride(0) if N > 1 else K
+    a = _lib.Norm(x.data_ptr(), None if residual is None else residual.data_ptr(),
+                  None if h is None else h.data_ptr(), w, xq.data_ptr(), amax.data_ptr(),
+                  xsum.data_ptr(), N, K, ldx, ldr, ldh, eps, ACT_DTYPES[x.dtype],
+                  1 if normalize else 0)
+    _lib.check(_launch(dev, stream, lambda s: _lib.load().bitlinear_norm_quant(a, s)),
+               "bitlinear_norm_quant")
+    return (xq, amax, xsum) if residual is None else (h, xq, amax, xsum)
+
+
+def gated_norm_quant(gate, up, weight=None, eps=1e-5, activation="silu", normalize=True,
+                     stream=None):
+    """The middle of a gated MLP: act(gate) * up, the norm (unless `normalize`
+    is false) and the int8 quantiser, in one launch.  gate and up: [N, K] of
+    one type with dense rows of any row stride, for instance the halves of one
+    [N, 2K] buffer.  Returns (xq, amax, xsum), the input of the down
+    projection."""
+    ldg = _need_rows(gate, "gate")
+    N, K = gate.shape
+    dev = gate.device
+    ldu = _need_rows(up, "up", (N, K), gate.dtype)
+    _on(dev, up=up)
+    act = _activation(activation)
+    w = _need_vector(weight, K, "weight", dev)
+    if weight is not None and not normalize:
+        raise ValueError("weight belongs to the norm: pass None without it")
+    with _out_stream(stream, dev):
+        xq, amax, xsum = _codes_out(N, K, dev)
+    a = _lib.GatedNorm(gate.data_ptr(), up.data_ptr(), w, xq.data_ptr(), amax.data_ptr(),
+                       xsum.data_ptr(), N, K, ldg, ldu, eps, ACT_DTYPES[gate.dtype], act,
+                       1 if normalize else 0)
+    _lib.check(_launch(dev, stream, lambda s: _lib.load().bitlinear_gated_norm_quant(a, s)),
+               "bitlinear_gated_norm_quant")
+    return xq, amax, xsum
+
+
+def _linear_entry(packed, alpha, xq, amax, xsum, bias, activation, residual, out_dtype, out,
+                  stream):
+    """Checks one layer of a linear call; returns its entry and its output."""
+    _need(packed, torch.int32, "packed")
+    _need(alpha, torch.float32, "alpha")
+    _need(xq, torch.int8, "xq")
+    N, K = xq.shape
+    M = packed.shape[0]
+    _check_token_vector(amax, N, torch.float32, "amax")
+    _check_token_vector(xsum, N, torch.int32, "xsum")
+    if packed.shape[1] != packed_row_words(K):
+        raise ValueError("packed must be [M, packed_row_words(K)] = [%d, %d], got %s"
+                         % (M, packed_row_words(K), tuple(packed.shape)))
+    dev = packed.device
+    _on(dev, alpha=alpha, xq=xq, amax=amax, xsum=xsum)
+    if out_dtype is None:
+        out_dtype = (out.dtype if out is not None else
+                     residual.dtype if residual is not None else torch.float32)
+    if out_dtype not in ACT_DTYPES:
+        raise TypeError("out_dtype must be float32, bfloat16 or float16, got %s" % out_dtype)
+    ldr = 0
+    if residual is not None:
+        ldr = _need_rows(residual, "residual", (N, M), out_dtype)
+        _on(dev, residual=residual)
+    if out is None:
+        with _out_stream(stream, dev):
+            out = torch.empty((N, M), dtype=out_dtype, device=dev)
+        ldy = M
+    else:
+        ldy = _need_rows(out, "out", (N, M), out_dtype)
+        _on(dev, out=out)
+    entry = (packed.data_ptr(), alpha.data_ptr(), M, K, xq.data_ptr(), amax.data_ptr(),
+             xsum.data_ptr(), _need_vector(bias, M, "bias", dev),
+             None if residual is None else residual.data_ptr(), out.data_ptr(), ldr, ldy,
+             ACT_DTYPES[out_dtype], _activation(activation))
+    return entry, out
+
+
+def linear(packed, alpha, xq, amax, xsum, bias=None, activation=None, residual=None,
+           out_dtype=None, out=None, stream=None):
+    """The ternary product with its epilogue, any token count:
+    act(y + bias) + residual, computed in fp32 and rounded once to out_dtype
+    (fp32, bf16 or fp16; by default the type of out, else of the residual,
+    else fp32).  bias: fp32 [M]; residual and out: [N, M] of out_dtype with
+    dense rows of any row stride; out may be the residual itself."""
+    entry, out = _linear_entry(packed, alpha, xq, amax, xsum, bias, activation, residual,
+                               out_dtype, out, stream)
+    arr = (_lib.LinearProblem * 1)(entry)
+    N = xq.shape[0]
+    _lib.check(_launch(packed.device, stream,
+                       lambda s: _lib.load().bitlinear_linear(arr, 1, N, s)),
+               "bitlinear_linear")
+    return out
+
+
+def linear_grouped(layers, xq, amax, xsum, bias=None, activation=None, residual=None,
+                   out_dtype=None, outs=None, stream=None):
+    """linear over several layers that share the token count, in one launch
+    (q, k and v; gate and up).  layers: list of (packed, alpha); every other
+    argument is one value for all layers or a list with one per layer.
+    Returns the list of outputs."""
+    n = len(layers)
+    if n == 0:
+        return []
+
+    def each(v, name):
+        v = list(v) if isinstance(v, (list, tuple)) else [v] * n
+        if len(v) != n:
+            raise ValueError("%s: one per layer, or one for all" % name)
+        return v
+
+    if outs is not None and not isinstance(outs, (list, tuple)):
+        raise ValueError("outs: one per layer")
+    cols = [each(v, k) for v, k in ((xq, "xq"), (amax, "amax"), (xsum, "xsum"), (bias, "bias"),
+                                    (activation, "activation"), (residual, "residual"),
+                                    (out_dtype, "out_dtype"), (outs, "outs"))]
+    N, dev = cols[0][0].shape[0], layers[0][0].device
+    arr, ys = (_lib.LinearProblem * n)(), []
+    for i, (packed, alpha) in enumerate(layers):
+        xqi, am, xs, b, act, res, dt, out = (c[i] for c in cols)
+        if xqi.shape[0] != N:
+            raise ValueError("layer %d: all layers share the token count" % i)
+        _on(dev, packed=packed)
+        entry, y = _linear_entry(packed, alpha, xqi, am, xs, b, act, res, dt, out, stream)
+        arr[i] = entry
+        ys.append(y)
+    _lib.check(_launch(dev, stream, lambda s: _lib.load().bitlinear_linear(arr, n, N, s)),
+               "bitlinear_linear")
+    return ys
+
+
+class TernaryLinear:
+    """A BitLinear layer: packed 2-bit ternary weights + alpha (and a bias, if
+    the layer has one), applied to fp32 activations: the fused quantise+GEMV
+    kernel below GEMM_MIN_TOKENS tokens, else quant_act -> tensor-core GEMM
+    with the fused rescale; with a bias, quant_act -> linear.  `quantized`
+    takes what norm_quant, gated_norm_quant or quant_act gave."""
+
+    def __init__(self, packed, alpha, in_features, out_features, bias=None):
+        self.packed, self.alpha, self.bias = packed, alpha, bias
         self.in_features, self.out_features = in_features, out_features
 
     @classmethod
-    def from_float(cls, W, stream=None):
+    def from_float(cls, W, stream=None, bias=None):
         packed, alpha = pack_weights(W, stream)
-        return cls(packed, alpha, W.shape[1], W.shape[0])
+        return cls(packed, alpha, W.shape[1], W.shape[0], bias)
+
+    def quantized(self, xq, amax, xsum, activation=None, residual=None, out_dtype=None, out=None,
+                  stream=None):
+        return linear(self.packed, self.alpha, xq, amax, xsum, self.bias, activation, residual,
+                      out_dtype, out, stream)
 
     def __call__(self, x, stream=None):
+        if self.bias is not None:
+            return self.quantized(*quant_act(x, stream), stream=stream)
         if use_fused_decode(x.shape[0], x.shape[1]):
             return gemv_quant(self.packed, self.alpha, x, self.out_features, stream=stream)
         xq, amax, xsum = quant_act(x, stream)

@@ -8,6 +8,7 @@
 #include <algorithm>
 #include <atomic>
 #include <climits>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -99,6 +100,24 @@ bool encode_u8_2d(CUtensorMap* map, const void* ptr, uint64_t cols, uint64_t row
   return r == CUDA_SUCCESS;
 }
 
+int64_t elem_bytes(int dtype) { return dtype == BITLINEAR_F32 ? 4 : 2; }
+bool known_dtype(int dtype) { return dtype >= BITLINEAR_F32 && dtype <= BITLINEAR_F16; }
+bool known_act(int act) { return act >= BITLINEAR_ACT_NONE && act <= BITLINEAR_ACT_GELU_TANH; }
+
+void fill_gemv(bl::GemvProblem& g, const bitlinear_problem& q, int64_t unit_begin) {
+  g.packed = q.packed;
+  g.alpha = q.alpha;
+  g.xq = q.xq;
+  g.amax = q.amax;
+  g.xsum = q.xsum;
+  g.y = q.y;
+  g.acc = q.acc;
+  g.M = static_cast<int>(q.M);
+  g.K = static_cast<int>(q.K);
+  g.W = static_cast<int>(packed_row_words(q.K));
+  g.unit_begin = static_cast<int>(unit_begin);
+}
+
 // Decode GEMV over problems that share N (all validated): one launch
 // per kGemvMaxProblems problems, units of 32 rows numbered across problems.
 bitlinear_status gemv_group(const bitlinear_problem* probs, int64_t count, int64_t N,
@@ -114,18 +133,7 @@ bitlinear_status gemv_group(const bitlinear_problem* probs, int64_t count, int64
     int64_t units = 0;
     for (int i = 0; i < n; ++i) {
       const bitlinear_problem& q = probs[base + i];
-      bl::GemvProblem& g = p.prob[i];
-      g.packed = q.packed;
-      g.alpha = q.alpha;
-      g.xq = q.xq;
-      g.amax = q.amax;
-      g.xsum = q.xsum;
-      g.y = q.y;
-      g.acc = q.acc;
-      g.M = static_cast<int>(q.M);
-      g.K = static_cast<int>(q.K);
-      g.W = static_cast<int>(packed_row_words(q.K));
-      g.unit_begin = static_cast<int>(units);
+      fill_gemv(p.prob[i], q, units);
       units += (q.M + bl::kGemvTileRows - 1) / bl::kGemvTileRows;
     }
     if (units > INT_MAX) return BITLINEAR_ERR_UNSUPPORTED_SHAPE;
@@ -179,31 +187,32 @@ void build_gemm_schedule(bl::GemmParams& p, int sms) {
   const int grid = p.total_tiles < sms ? p.total_tiles : sms;
   p.use_sched = 0;
   if (grid > bl::kGemmMaxGrid || p.total_tiles > bl::kGemmMaxSched || p.num_problems < 2) return;
-  std::vector<std::pair<int64_t, int>> heap;   // (load, cta), min-heap
-  heap.reserve(grid);
-  for (int c = 0; c < grid; ++c) heap.push_back({0, c});
-  std::vector<int> owner(p.total_tiles);
-  std::vector<int> count(grid, 0);
+  std::pair<int64_t, int> heap[bl::kGemmMaxGrid];   // (load, cta), min-heap
+  uint8_t owner[bl::kGemmMaxSched];                 // CTA of each tile
+  int count[bl::kGemmMaxGrid] = {};
+  static_assert(bl::kGemmMaxGrid <= 256, "owner entries");
+  for (int c = 0; c < grid; ++c) heap[c] = {0, c};
   auto cmp = [](const std::pair<int64_t, int>& a, const std::pair<int64_t, int>& b) {
     return a.first != b.first ? a.first > b.first : a.second > b.second;
   };
-  std::make_heap(heap.begin(), heap.end(), cmp);
+  std::make_heap(heap, heap + grid, cmp);
   for (int pi = 0; pi < p.num_problems; ++pi) {
     const bl::GemmProblem& g = p.prob[pi];
     const int end = pi + 1 < p.num_problems ? p.prob[pi + 1].tile_begin : p.total_tiles;
     for (int t = g.tile_begin; t < end; ++t) {
-      std::pop_heap(heap.begin(), heap.end(), cmp);
-      auto& least = heap.back();
-      owner[t] = least.second;
+      std::pop_heap(heap, heap + grid, cmp);
+      auto& least = heap[grid - 1];
+      owner[t] = static_cast<uint8_t>(least.second);
       count[least.second] += 1;
       least.first += g.K;
-      std::push_heap(heap.begin(), heap.end(), cmp);
+      std::push_heap(heap, heap + grid, cmp);
     }
   }
   p.sched_begin[0] = 0;
   for (int c = 0; c < grid; ++c)
     p.sched_begin[c + 1] = static_cast<uint16_t>(p.sched_begin[c] + count[c]);
-  std::vector<int> fill(p.sched_begin, p.sched_begin + grid);
+  int fill[bl::kGemmMaxGrid];
+  std::copy(p.sched_begin, p.sched_begin + grid, fill);
   for (int pi = 0; pi < p.num_problems; ++pi) {
     const bl::GemmProblem& g = p.prob[pi];
     const int end = pi + 1 < p.num_problems ? p.prob[pi + 1].tile_begin : p.total_tiles;
@@ -215,14 +224,21 @@ void build_gemm_schedule(bl::GemmParams& p, int sms) {
   p.use_sched = 1;
 }
 
+bl::Epilogue epilogue_of(const bitlinear_linear_problem& q) {
+  return {q.bias, q.residual, q.y, q.ldr, q.ldy, q.dtype, q.activation};
+}
+
 // Tensor-core GEMM over problems that share N (all validated): one
 // persistent launch per kGemmMaxProblems problems, tiles numbered across
 // problems with the largest K first so the longest tiles start in the first
 // wave.  Ragged edges come from the tensor maps: loads past M, K or N read
 // zeros, and stores past M or N are dropped.  A y whose row pitch (4M bytes)
 // is not a multiple of 16 cannot be a TMA tensor; its epilogue stores directly.
+// `lin`: the epilogues of the same problems (bitlinear_linear), whose outputs
+// take no tensor map; null otherwise.
+template <class Params>
 bitlinear_status gemm_group(const bitlinear_problem* probs, int64_t count, int64_t N,
-                            cudaStream_t s) {
+                            cudaStream_t s, const bitlinear_linear_problem* lin = nullptr) {
   DeviceInfo* dev = nullptr;
   bitlinear_status st = device_info(&dev);
   if (st != BITLINEAR_OK) return st;
@@ -248,12 +264,13 @@ bitlinear_status gemm_group(const bitlinear_problem* probs, int64_t count, int64
         order[j] = order[j - 1];
         order[j - 1] = t;
       }
-    bl::GemmParams p;
-    memset(&p, 0, sizeof p);
+    Params p;
+    memset(static_cast<void*>(&p), 0, sizeof p);
     int64_t tiles = 0;
     for (int i = 0; i < n; ++i) {
       const bitlinear_problem& q = probs[base + order[i]];
-      const bool direct = small || q.M % 4 != 0;   // the small kernel stores directly
+      // the small kernel and the epilogues store directly
+      const bool direct = small || Params::kEpilogue || q.M % 4 != 0;
       // packed weights: one k-block (32 bytes) per row, or for the small kernel
       // four k-blocks (128 bytes, swizzled) per row
       if (!encode_u8_2d(&p.tmA[i], q.packed, static_cast<uint64_t>(packed_row_words(q.K) * 4),
@@ -278,6 +295,7 @@ bitlinear_status gemm_group(const bitlinear_problem* probs, int64_t count, int64
       g.n_tiles = static_cast<int>(n_tiles);
       g.tile_begin = static_cast<int>(tiles);
       g.direct_store = direct ? 1 : 0;
+      if constexpr (Params::kEpilogue) p.ep[i] = epilogue_of(lin[base + order[i]]);
       tiles += (q.M + BMt - 1) / BMt * n_tiles;
     }
     if (tiles > INT_MAX) return BITLINEAR_ERR_UNSUPPORTED_SHAPE;
@@ -285,9 +303,99 @@ bitlinear_status gemm_group(const bitlinear_problem* probs, int64_t count, int64
     p.total_tiles = static_cast<int>(tiles);
     p.wait_ns = blh::wait_limit_ns();
     build_gemm_schedule(p, wide ? dev->sms / 2 : dev->sms);
-    st = blh::launch_gemm(small ? (BN == 16 ? 4 : 5) : wide ? 1 : BN == 64 ? 3 : 0, p, dev, s);
+    const int variant = small ? (BN == 16 ? 4 : 5) : wide ? 1 : BN == 64 ? 3 : 0;
+    if constexpr (Params::kEpilogue)
+      st = blh::launch_gemm_ep(variant, p, dev, s);
+    else
+      st = blh::launch_gemm(variant, p, dev, s);
     if (st != BITLINEAR_OK) return st;
   }
+  return BITLINEAR_OK;
+}
+
+// ---- products with an epilogue
+
+bitlinear_status check_linear_problem(const bitlinear_linear_problem& q, int64_t N) {
+  bitlinear_status st = check_mk(q.M, q.K);
+  if (st != BITLINEAR_OK) return st;
+  if (N > INT_MAX / 2) return BITLINEAR_ERR_UNSUPPORTED_SHAPE;
+  if (!q.packed || !q.alpha || !q.xq || !q.amax || !q.xsum || !q.y)
+    return BITLINEAR_ERR_INVALID_ARG;
+  if (!known_dtype(q.dtype) || !known_act(q.activation)) return BITLINEAR_ERR_INVALID_ARG;
+  if (N > 1 && (q.ldy < q.M || (q.residual && q.ldr < q.M))) return BITLINEAR_ERR_INVALID_ARG;
+  if (N > 1 && q.residual == q.y && q.ldr != q.ldy) return BITLINEAR_ERR_INVALID_ARG;
+  if (!aligned16(q.packed) || !aligned16(q.xq)) return BITLINEAR_ERR_MISALIGNED;
+  if (!aligned4(q.alpha) || !aligned4(q.amax) || !aligned4(q.xsum) || !aligned4(q.bias))
+    return BITLINEAR_ERR_MISALIGNED;
+  const uintptr_t e = static_cast<uintptr_t>(elem_bytes(q.dtype) - 1);
+  if ((reinterpret_cast<uintptr_t>(q.y) & e) || (reinterpret_cast<uintptr_t>(q.residual) & e))
+    return BITLINEAR_ERR_MISALIGNED;
+  return BITLINEAR_OK;
+}
+
+bitlinear_problem product_of(const bitlinear_linear_problem& q) {
+  return {q.packed, q.alpha, q.M, q.K, q.xq, q.amax, q.xsum, nullptr, nullptr};
+}
+
+// Validated problems sharing N.  One token takes the GEMV (one launch per
+// kGemvEpMaxProblems problems), more the tensor cores.
+bitlinear_status linear_group(const bitlinear_linear_problem* probs, int64_t count, int64_t N,
+                              cudaStream_t s) {
+  DeviceInfo* dev = nullptr;
+  bitlinear_status st = device_info(&dev);
+  if (st != BITLINEAR_OK) return st;
+  if (N > 1) {
+    bitlinear_problem products[bl::kGemmMaxProblems];
+    for (int64_t base = 0; base < count; base += bl::kGemmMaxProblems) {
+      const int64_t n = std::min<int64_t>(count - base, bl::kGemmMaxProblems);
+      for (int64_t i = 0; i < n; ++i) products[i] = product_of(probs[base + i]);
+      st = gemm_group<bl::GemmEpParams>(products, n, N, s, probs + base);
+      if (st != BITLINEAR_OK) return st;
+    }
+    return BITLINEAR_OK;
+  }
+  for (int64_t base = 0; base < count; base += bl::kGemvEpMaxProblems) {
+    const int n = static_cast<int>(std::min<int64_t>(count - base, bl::kGemvEpMaxProblems));
+    bl::GemvEpParams p;
+    int64_t units = 0;
+    for (int i = 0; i < n; ++i) {
+      const bitlinear_linear_problem& q = probs[base + i];
+      fill_gemv(p.prob[i], product_of(q), units);
+      p.prob[i].ep = epilogue_of(q);
+      units += (q.M + bl::kGemvTileRows - 1) / bl::kGemvTileRows;
+      if (units > INT_MAX) return BITLINEAR_ERR_UNSUPPORTED_SHAPE;
+    }
+    p.num_problems = n;
+    p.total_units = static_cast<int>(units);
+    if ((st = blh::launch_gemv_ep(p, dev, s)) != BITLINEAR_OK) return st;
+  }
+  return BITLINEAR_OK;
+}
+
+// ---- row operators between two products
+
+// What the norm calls share: sizes, outputs, eps and weight.
+bitlinear_status check_norm(int64_t N, int64_t K, int dtype, int normalize, double eps,
+                            const float* weight, const int8_t* xq, const float* amax,
+                            const int32_t* xsum) {
+  if (N < 0 || K < 0) return BITLINEAR_ERR_INVALID_ARG;
+  if (K == 0 || K % 16 != 0 || K > kMaxK || N > INT_MAX) return BITLINEAR_ERR_UNSUPPORTED_SHAPE;
+  if (!known_dtype(dtype)) return BITLINEAR_ERR_INVALID_ARG;
+  if (normalize ? !(eps > 0.0 && std::isfinite(eps)) : weight != nullptr)
+    return BITLINEAR_ERR_INVALID_ARG;
+  if (N == 0) return BITLINEAR_OK;
+  if (!xq || !amax) return BITLINEAR_ERR_INVALID_ARG;
+  if (!aligned16(weight) || !aligned16(xq) || !aligned4(amax) || !aligned4(xsum))
+    return BITLINEAR_ERR_MISALIGNED;
+  return BITLINEAR_OK;
+}
+
+// An activation matrix read or written in 16-byte pieces.
+bitlinear_status check_rows(const void* p, int64_t ld, int64_t N, int64_t K, int dtype) {
+  if (!p) return BITLINEAR_ERR_INVALID_ARG;
+  if (N > 1 && ld < K) return BITLINEAR_ERR_INVALID_ARG;
+  if (!aligned16(p) || (N > 1 && ld * elem_bytes(dtype) % 16 != 0))
+    return BITLINEAR_ERR_MISALIGNED;
   return BITLINEAR_OK;
 }
 
@@ -647,7 +755,7 @@ bitlinear_status bitlinear_gemm(const uint32_t* packed, const float* alpha, int6
   bitlinear_status st = check_matmul_args(packed, alpha, M, K, xq, amax, xsum, N, y, acc);
   if (st != BITLINEAR_OK || N == 0) return st;
   const bitlinear_problem q = {packed, alpha, M, K, xq, amax, xsum, y, acc};
-  return gemm_group(&q, 1, N, reinterpret_cast<cudaStream_t>(stream));
+  return gemm_group<bl::GemmParams>(&q, 1, N, reinterpret_cast<cudaStream_t>(stream));
 }
 
 bitlinear_status bitlinear_gemm_grouped(const bitlinear_problem* problems, int64_t count,
@@ -658,7 +766,7 @@ bitlinear_status bitlinear_gemm_grouped(const bitlinear_problem* problems, int64
     bitlinear_status st = check_problem(problems[i], N);
     if (st != BITLINEAR_OK) return st;
   }
-  return gemm_group(problems, count, N, reinterpret_cast<cudaStream_t>(stream));
+  return gemm_group<bl::GemmParams>(problems, count, N, reinterpret_cast<cudaStream_t>(stream));
 }
 
 bitlinear_status bitlinear_gemv_quant(const uint32_t* packed, const float* alpha, int64_t M,
@@ -684,6 +792,56 @@ bitlinear_status bitlinear_gemv_quant_grouped(const bitlinear_fused_problem* pro
     if (st != BITLINEAR_OK) return st;
   }
   return gemv_quant_group(problems, count, N, reinterpret_cast<cudaStream_t>(stream));
+}
+
+bitlinear_status bitlinear_linear(const bitlinear_linear_problem* problems, int64_t count,
+                                  int64_t N, bitlinear_stream_t stream) {
+  if (count < 0 || N < 0 || (count > 0 && !problems)) return BITLINEAR_ERR_INVALID_ARG;
+  if (count == 0 || N == 0) return BITLINEAR_OK;
+  for (int64_t i = 0; i < count; ++i) {
+    const bitlinear_status st = check_linear_problem(problems[i], N);
+    if (st != BITLINEAR_OK) return st;
+  }
+  return linear_group(problems, count, N, reinterpret_cast<cudaStream_t>(stream));
+}
+
+bitlinear_status bitlinear_norm_quant(const bitlinear_norm* a, bitlinear_stream_t stream) {
+  if (!a) return BITLINEAR_ERR_INVALID_ARG;
+  bitlinear_status st = check_norm(a->N, a->K, a->dtype, a->normalize, a->eps, a->weight, a->xq,
+                                   a->amax, a->xsum);
+  if (st != BITLINEAR_OK || a->N == 0) return st;
+  if ((st = check_rows(a->x, a->ldx, a->N, a->K, a->dtype)) != BITLINEAR_OK) return st;
+  if (!a->residual != !a->h) return BITLINEAR_ERR_INVALID_ARG;
+  if (a->residual) {
+    if ((st = check_rows(a->residual, a->ldr, a->N, a->K, a->dtype)) != BITLINEAR_OK) return st;
+    if ((st = check_rows(a->h, a->ldh, a->N, a->K, a->dtype)) != BITLINEAR_OK) return st;
+    if (a->N > 1 && ((a->h == a->residual && a->ldh != a->ldr) ||
+                     (a->h == a->x && a->ldh != a->ldx)))
+      return BITLINEAR_ERR_INVALID_ARG;
+  }
+  const bl::NormParams p = {a->x,   a->residual, a->h,   a->weight, a->xq,
+                            a->amax, a->xsum,    a->ldx, a->ldr,    a->ldh,
+                            a->eps, static_cast<int>(a->K), a->normalize ? 1 : 0,
+                            BITLINEAR_ACT_NONE};
+  return blh::launch_norm(false, static_cast<int>(a->N), a->dtype, p,
+                          reinterpret_cast<cudaStream_t>(stream));
+}
+
+bitlinear_status bitlinear_gated_norm_quant(const bitlinear_gated_norm* a,
+                                            bitlinear_stream_t stream) {
+  if (!a) return BITLINEAR_ERR_INVALID_ARG;
+  bitlinear_status st = check_norm(a->N, a->K, a->dtype, a->normalize, a->eps, a->weight, a->xq,
+                                   a->amax, a->xsum);
+  if (st == BITLINEAR_OK && !known_act(a->activation)) st = BITLINEAR_ERR_INVALID_ARG;
+  if (st != BITLINEAR_OK || a->N == 0) return st;
+  if ((st = check_rows(a->gate, a->ldg, a->N, a->K, a->dtype)) != BITLINEAR_OK) return st;
+  if ((st = check_rows(a->up, a->ldu, a->N, a->K, a->dtype)) != BITLINEAR_OK) return st;
+  const bl::NormParams p = {a->gate, a->up,   nullptr, a->weight, a->xq,
+                            a->amax, a->xsum, a->ldg,  a->ldu,    0,
+                            a->eps,  static_cast<int>(a->K), a->normalize ? 1 : 0,
+                            a->activation};
+  return blh::launch_norm(true, static_cast<int>(a->N), a->dtype, p,
+                          reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t bitlinear_tl2_row_bytes(int64_t K) {

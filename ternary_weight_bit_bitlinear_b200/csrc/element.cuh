@@ -1,0 +1,93 @@
+// element.cuh -- element types of activation matrices (fp32, bf16, fp16) and
+// the pointwise activations, shared by the kernels around the products
+// (norm.cuh, epilogue.cuh).  Everything is computed in fp32: a value read is
+// widened exactly, a value written is rounded once, to nearest even.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "bitlinear.h"
+
+namespace bl {
+
+template <typename T>
+struct Elem;
+
+template <>
+struct Elem<float> {
+  static __device__ __forceinline__ float to_float(float v) { return v; }
+  static __device__ __forceinline__ float from_float(float v) { return v; }
+};
+template <>
+struct Elem<__nv_bfloat16> {
+  static __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+  static __device__ __forceinline__ __nv_bfloat16 from_float(float v) {
+    return __float2bfloat16_rn(v);
+  }
+};
+template <>
+struct Elem<__half> {
+  static __device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
+  static __device__ __forceinline__ __half from_float(float v) { return __float2half_rn(v); }
+};
+
+// Elements of one 16-byte access.
+template <typename T>
+constexpr int kVec = 16 / static_cast<int>(sizeof(T));
+
+template <typename T>
+union Vec16 {
+  uint4 u;
+  T e[kVec<T>];
+};
+
+template <typename T>
+__device__ __forceinline__ void load_vec(const T* p, float (&f)[kVec<T>]) {
+  Vec16<T> v;
+  v.u = *reinterpret_cast<const uint4*>(p);
+#pragma unroll
+  for (int i = 0; i < kVec<T>; ++i) f[i] = Elem<T>::to_float(v.e[i]);
+}
+
+// Stores f rounded to T and leaves the rounded values in f.
+template <typename T>
+__device__ __forceinline__ void store_vec(T* p, float (&f)[kVec<T>]) {
+  Vec16<T> v;
+#pragma unroll
+  for (int i = 0; i < kVec<T>; ++i) {
+    v.e[i] = Elem<T>::from_float(f[i]);
+    f[i] = Elem<T>::to_float(v.e[i]);
+  }
+  *reinterpret_cast<uint4*>(p) = v.u;
+}
+
+// act(v), every operation a single fp32 rounding (no contraction):
+//   relu   max(v, 0)          relu2  max(v, 0)^2
+//   silu   v / (1 + e^-v)
+//   gelu   0.5 v (1 + erf(v / sqrt 2))
+//   gelu_tanh  0.5 v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3)))
+// A NaN stays a NaN.
+__device__ __forceinline__ float activate(float v, int act) {
+  switch (act) {
+    case BITLINEAR_ACT_RELU: return v < 0.0f ? 0.0f : v;
+    case BITLINEAR_ACT_RELU2: {
+      const float r = v < 0.0f ? 0.0f : v;
+      return __fmul_rn(r, r);
+    }
+    case BITLINEAR_ACT_SILU: return __fdiv_rn(v, __fadd_rn(1.0f, expf(-v)));
+    case BITLINEAR_ACT_GELU:
+      return __fmul_rn(__fmul_rn(0.5f, v),
+                       __fadd_rn(1.0f, erff(__fmul_rn(v, 0.7071067811865476f))));
+    case BITLINEAR_ACT_GELU_TANH: {
+      const float c = __fmul_rn(__fmul_rn(__fmul_rn(0.044715f, v), v), v);
+      const float t = tanhf(__fmul_rn(0.7978845608028654f, __fadd_rn(v, c)));
+      return __fmul_rn(__fmul_rn(0.5f, v), __fadd_rn(1.0f, t));
+    }
+    default: return v;
+  }
+}
+
+}  // namespace bl

@@ -27,6 +27,7 @@
 // persistent launch: tiles are numbered across problems.
 #pragma once
 
+#include "epilogue.cuh"
 #include "ptx.cuh"
 
 namespace bl {
@@ -54,6 +55,7 @@ struct GemmProblem {
 };
 
 struct GemmParams {
+  static constexpr bool kEpilogue = false;
   CUtensorMap tmA[kGemmMaxProblems];   // packed weights as uint8 [M][row bytes], box 32 x 128
   CUtensorMap tmB[kGemmMaxProblems];   // xq as uint8 [N][K], box 128 x BN, 128B swizzle
   CUtensorMap tmY[kGemmMaxProblems];   // y as fp32 [N][M], box 32 x 32
@@ -69,6 +71,14 @@ struct GemmParams {
   uint32_t sched[kGemmMaxSched];   // gemm_sched_entry(problem, m_blk, n_blk)
 };
 static_assert(sizeof(GemmParams) <= 32764, "kernel parameter space");
+
+// The same launch for bitlinear_linear: each problem carries its epilogue
+// (tmY, y and acc are not used).
+struct GemmEpParams : GemmParams {
+  static constexpr bool kEpilogue = true;
+  Epilogue ep[kGemmMaxProblems];
+};
+static_assert(sizeof(GemmEpParams) <= 32764, "kernel parameter space");
 
 // A schedule entry packs a tile's problem, row block and token block, so a
 // CTA finds its tile with two parameter loads (begin, entry) instead of a
@@ -117,6 +127,20 @@ struct GemmSmem {
   int abort;
 };
 
+// Epilogue of one 32-token x 32-row block (r: this lane's row m, tokens n0
+// ..): the rescaled accumulators go through this warp's staging block so that
+// the rest runs as a loop over tokens (each lane reads back what it wrote).
+__device__ __forceinline__ void gemm_ep_block(const Epilogue& ep, const uint32_t (&r)[32],
+                                              const int* xs, const float* sc, float* blk, int n0,
+                                              int N, int m, int M, int lane) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j)
+    blk[j * 32 + lane] = __fmul_rn(__int2float_rn(static_cast<int>(r[j]) - xs[j]), sc[j]);
+  if (m >= M) return;
+#pragma unroll 4
+  for (int j = 0; j < min(32, N - n0); ++j) ep_element(ep, n0 + j, m, blk[j * 32 + lane]);
+}
+
 // Before the CTA releases its shared memory: wait for the TMA loads still in
 // flight.  Only the last STAGES loads issued can be (the producer waited for
 // each stage to be consumed before refilling it); load i completes phase
@@ -161,9 +185,9 @@ __device__ __forceinline__ void gemm_tile_at(const GemmParams& p, int i, int& pi
                    n_blk);
 }
 
-template <int BN, int STAGES>
+template <int BN, int STAGES, class P>
 __global__ void __launch_bounds__(kGemmThreads, 1)
-gemm_i8_tcgen05_kernel(const __grid_constant__ GemmParams p) {
+gemm_i8_tcgen05_kernel(const __grid_constant__ P p) {
   extern __shared__ uint8_t smem_raw[];
   using Smem = GemmSmem<BN, STAGES>;
   const uint32_t base = smem_u32(smem_raw);
@@ -375,6 +399,11 @@ gemm_i8_tcgen05_kernel(const __grid_constant__ GemmParams p) {
         tmem_ld_wait();
         const int n0 = n_blk * BN + cc * 32;
         if (n0 >= pr.N) continue;          // tokens past N: nothing to store
+        if constexpr (P::kEpilogue) {
+          gemm_ep_block(p.ep[pi], r, xs + (cc >> 1) * 32, sc + (cc >> 1) * 32, s.ep_out[e], n0,
+                        pr.N, m, pr.M, lane);
+          continue;
+        }
         if (pr.direct_store) {   // rows past M and tokens past N are not stored
 #pragma unroll
           for (int j = 0; j < 32; ++j) {

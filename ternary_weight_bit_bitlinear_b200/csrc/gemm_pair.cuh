@@ -59,9 +59,9 @@ struct GemmPairSmem {
   int abort;
 };
 
-template <int STAGES>
+template <int STAGES, class P>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
-gemm_i8_pair_kernel(const __grid_constant__ GemmParams p) {
+gemm_i8_pair_kernel(const __grid_constant__ P p) {
   extern __shared__ uint8_t smem_raw[];
   using Smem = GemmPairSmem<STAGES>;
   const uint32_t base = smem_u32(smem_raw);
@@ -288,6 +288,11 @@ gemm_i8_pair_kernel(const __grid_constant__ GemmParams p) {
         tmem_ld_wait();
         const int n0 = n_blk * kPairBN + cc * 32;
         if (n0 >= pr.N) continue;          // tokens past N: nothing to store
+        if constexpr (P::kEpilogue) {
+          gemm_ep_block(p.ep[pi], r, xs + (cc >> 1) * 32, sc + (cc >> 1) * 32, s.ep_out[e], n0,
+                        pr.N, m, pr.M, lane);
+          continue;
+        }
         if (pr.direct_store) {   // rows past M and tokens past N are not stored
 #pragma unroll
           for (int j = 0; j < 32; ++j) {

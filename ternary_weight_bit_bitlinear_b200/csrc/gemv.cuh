@@ -25,6 +25,7 @@
 // the inner loop and no cross-lane reduction at all.
 #pragma once
 
+#include "epilogue.cuh"
 #include "ptx.cuh"
 
 namespace bl {
@@ -36,6 +37,7 @@ constexpr int kGemvWarps = 4;            // warps per CTA
 constexpr int kGemvThreads = kGemvWarps * 32;
 constexpr int kGemvMaxTokens = 16;
 constexpr int kGemvMaxProblems = 256;
+constexpr int kGemvEpMaxProblems = 64;
 
 template <int NT>
 struct GemvCfg {
@@ -59,12 +61,25 @@ struct GemvProblem {
 };
 
 struct GemvParams {
+  static constexpr bool kEpilogue = false;
   GemvProblem prob[kGemvMaxProblems];
   int num_problems;
   int total_units;
 };
 
-__device__ __forceinline__ int gemv_locate(const GemvParams& p, int unit) {
+// The same launch for bitlinear_linear: each problem carries its epilogue.
+struct GemvEpProblem : GemvProblem {
+  Epilogue ep;
+};
+struct GemvEpParams {
+  static constexpr bool kEpilogue = true;
+  GemvEpProblem prob[kGemvEpMaxProblems];
+  int num_problems;
+  int total_units;
+};
+
+template <class P>
+__device__ __forceinline__ int gemv_locate(const P& p, int unit) {
   int lo = 0, hi = p.num_problems - 1;
   while (lo < hi) {   // last problem whose unit_begin <= unit
     const int mid = (lo + hi + 1) >> 1;
@@ -158,9 +173,29 @@ __device__ __forceinline__ void gemv_chunk_dot(const uint8_t* wrow, uint32_t sw,
   }
 }
 
-template <int NT>
+// This lane's row, every token: sums to outputs.
+template <class P, int NT, class Problem>
+__device__ __forceinline__ void gemv_finish(const Problem& pr, int row, const int (&acc)[NT][4]) {
+  const float alpha = *pr.alpha;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int a = acc[t][0] + (acc[t][1] >> 2) + (acc[t][2] >> 4) + (acc[t][3] >> 6) -
+                  pr.xsum[t];
+    const float scale = __fmul_rn(alpha, __fdiv_rn(pr.amax[t], 127.0f));
+    const float v = __fmul_rn(__int2float_rn(a), scale);
+    if constexpr (P::kEpilogue) {
+      ep_element(pr.ep, t, row, v);
+    } else {
+      const int64_t o = static_cast<int64_t>(t) * pr.M + row;
+      pr.y[o] = v;
+      if (pr.acc) pr.acc[o] = a;
+    }
+  }
+}
+
+template <int NT, class P>
 __global__ void __launch_bounds__(kGemvThreads)
-gemv_tile_kernel(const __grid_constant__ GemvParams p) {
+gemv_tile_kernel(const __grid_constant__ P p) {
   using C = GemvCfg<NT>;
   extern __shared__ __align__(128) uint8_t smem[];
   pdl_wait_prior_grid();
@@ -206,7 +241,7 @@ gemv_tile_kernel(const __grid_constant__ GemvParams p) {
   int cslot = 0;
   for (int cu = blockIdx.x * kGemvWarps + warp; cu < p.total_units; cu += stride) {
     // by value: registers, not re-read from parameter space after each store
-    const GemvProblem pr = p.prob[gemv_locate(p, cu)];
+    const auto pr = p.prob[gemv_locate(p, cu)];
     const int row0 = (cu - pr.unit_begin) * kGemvTileRows;
     const int nchunks = (pr.K + kGemvChunkK - 1) / kGemvChunkK;
 
@@ -227,18 +262,7 @@ gemv_tile_kernel(const __grid_constant__ GemvParams p) {
     }
 
     const int row = row0 + lane;
-    if (row < pr.M) {
-      const float alpha = *pr.alpha;
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const int a = acc[t][0] + (acc[t][1] >> 2) + (acc[t][2] >> 4) + (acc[t][3] >> 6) -
-                      pr.xsum[t];
-        const float scale = __fmul_rn(alpha, __fdiv_rn(pr.amax[t], 127.0f));
-        const int64_t o = static_cast<int64_t>(t) * pr.M + row;
-        pr.y[o] = __fmul_rn(__int2float_rn(a), scale);
-        if (pr.acc) pr.acc[o] = a;
-      }
-    }
+    if (row < pr.M) gemv_finish<P>(pr, row, acc);
   }
   cp_async_wait<0>();
 }

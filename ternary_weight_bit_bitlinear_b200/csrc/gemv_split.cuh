@@ -13,16 +13,16 @@ namespace bl {
 // its C through its own ring (same layout, copies and arithmetic), the other
 // warps leave their int32 sums in their rings, and warp 0 adds them (integers:
 // the order does not matter) and writes y as gemv_tile_kernel does.
-template <int NT>
+template <int NT, class P>
 __global__ void __launch_bounds__(kGemvThreads)
-gemv_split_kernel(const __grid_constant__ GemvParams p) {
+gemv_split_kernel(const __grid_constant__ P p) {
   using C = GemvCfg<NT>;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* ring = smem + warp * C::kWarpBytes;
   const uint32_t sw = static_cast<uint32_t>(lane & 7);
   const int unit = blockIdx.x;
-  const GemvProblem pr = p.prob[gemv_locate(p, unit)];
+  const auto pr = p.prob[gemv_locate(p, unit)];
   const int row0 = (unit - pr.unit_begin) * kGemvTileRows;
   const int nchunks = (pr.K + kGemvChunkK - 1) / kGemvChunkK;
   const int kc0 = nchunks * warp / kGemvWarps, kc1 = nchunks * (warp + 1) / kGemvWarps;
@@ -87,18 +87,7 @@ gemv_split_kernel(const __grid_constant__ GemvParams p) {
       for (int j = 0; j < 4; ++j) acc[t][j] += o[(t * 4 + j) * 32 + lane];
   }
   const int row = row0 + lane;
-  if (row < pr.M) {
-    const float alpha = *pr.alpha;
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int a = acc[t][0] + (acc[t][1] >> 2) + (acc[t][2] >> 4) + (acc[t][3] >> 6) -
-                    pr.xsum[t];
-      const float scale = __fmul_rn(alpha, __fdiv_rn(pr.amax[t], 127.0f));
-      const int64_t o = static_cast<int64_t>(t) * pr.M + row;
-      pr.y[o] = __fmul_rn(__int2float_rn(a), scale);
-      if (pr.acc) pr.acc[o] = a;
-    }
-  }
+  if (row < pr.M) gemv_finish<P>(pr, row, acc);
 }
 
 }  // namespace bl

@@ -18,6 +18,7 @@
 #include "gemm_pair.cuh"
 #include "gemv.cuh"
 #include "gemv_quant.cuh"
+#include "norm.cuh"
 #include "tl2.cuh"
 
 namespace blh {
@@ -27,7 +28,7 @@ constexpr int kMaxDevices = 64;
 // Per-device facts and one-time set-up flags, looked up once per device.
 struct DeviceInfo {
   int sms = 0;
-  bool gemm_attr_set[8] = {};
+  bool gemm_attr_set[16] = {};
   int gemv_blocks_per_sm[bl::kGemvMaxTokens + 1] = {};   // 0: not set up yet
   int tl2_blocks_per_sm[bl::kGemvMaxTokens + 1] = {};    // 0: not set up yet
   bool gq_attr_set[bl::kGemvMaxTokens + 1] = {};
@@ -35,6 +36,8 @@ struct DeviceInfo {
   int gq_area[bl::kGemvMaxTokens + 1][bl::kGqMaxWarps + 1] = {};   // last shared-memory size
   int gq_occ[bl::kGemvMaxTokens + 1][bl::kGqMaxWarps + 1] = {};    // and its CTAs per SM
   bool gemv_split_attr_set[bl::kGemvMaxTokens + 1] = {};
+  int gemv_ep_blocks_per_sm = 0;      // 0: not set up yet
+  bool gemv_ep_split_attr_set = false;
 };
 
 // The calling thread's current device.
@@ -69,6 +72,13 @@ inline bitlinear_status launch_status() {
 // launch_gemv.cu: decode GEMV on int8 activations (tile or split-unit kernel).
 bitlinear_status launch_gemv(int N, const bl::GemvParams& p, DeviceInfo* dev, cudaStream_t s);
 
+// The one-token launch of bitlinear_linear (same kernels, with the epilogue).
+bitlinear_status launch_gemv_ep(const bl::GemvEpParams& p, DeviceInfo* dev, cudaStream_t s);
+
+// launch_norm.cu: row operators between two products, one CTA per row.
+bitlinear_status launch_norm(bool gated, int rows, int dtype, const bl::NormParams& p,
+                             cudaStream_t s);
+
 // launch_gemv_quant.cu: the fused quantise + GEMV decode kernel.  CTAs of
 // `warps` warps with `area` bytes of dynamic shared memory each.
 bitlinear_status gemv_quant_occupancy(int N, int warps, int area, DeviceInfo* dev, int* out);
@@ -80,6 +90,9 @@ bitlinear_status gemv_quant_launch(int N, int grid, int warps, const bl::GqParam
 // 5 = 32 tokens (A in tensor memory).
 bitlinear_status launch_gemm(int variant, const bl::GemmParams& p, DeviceInfo* dev,
                              cudaStream_t s);
+
+bitlinear_status launch_gemm_ep(int variant, const bl::GemmEpParams& p, DeviceInfo* dev,
+                                cudaStream_t s);
 
 // launch_tl2.cu: TL2-style storage.
 bitlinear_status launch_gemv_tl2(int N, const bl::Tl2Params& p, DeviceInfo* dev,

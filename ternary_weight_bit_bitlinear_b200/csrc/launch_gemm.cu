@@ -7,10 +7,16 @@
 namespace blh {
 namespace {
 
-template <int BN, int STAGES>
-bitlinear_status launch_single(const bl::GemmParams& p, DeviceInfo* dev, int slot,
-                               cudaStream_t s) {
-  auto kernel = bl::gemm_i8_tcgen05_kernel<BN, STAGES>;
+// Slot of DeviceInfo::gemm_attr_set: the variant, plus 8 with an epilogue.
+template <class P>
+constexpr int attr_slot(int variant) {
+  return variant + (P::kEpilogue ? 8 : 0);
+}
+
+template <int BN, int STAGES, class P>
+bitlinear_status launch_single(const P& p, DeviceInfo* dev, int variant, cudaStream_t s) {
+  const int slot = attr_slot<P>(variant);
+  auto kernel = bl::gemm_i8_tcgen05_kernel<BN, STAGES, P>;
   const int smem = static_cast<int>(sizeof(bl::GemmSmem<BN, STAGES>)) + 1024;
   if (!dev->gemm_attr_set[slot]) {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
@@ -26,15 +32,16 @@ bitlinear_status launch_single(const bl::GemmParams& p, DeviceInfo* dev, int slo
 
 // CTA-pair GEMM for wide token blocks: two CTAs (a compile-time cluster) per
 // 256 x 256 tile, one pair per two SMs.
-template <int STAGES>
-bitlinear_status launch_pair(const bl::GemmParams& p, DeviceInfo* dev, cudaStream_t s) {
-  auto kernel = bl::gemm_i8_pair_kernel<STAGES>;
+template <int STAGES, class P>
+bitlinear_status launch_pair(const P& p, DeviceInfo* dev, cudaStream_t s) {
+  const int slot = attr_slot<P>(1);
+  auto kernel = bl::gemm_i8_pair_kernel<STAGES, P>;
   const int smem = static_cast<int>(sizeof(bl::GemmPairSmem<STAGES>)) + 1024;
-  if (!dev->gemm_attr_set[1]) {
+  if (!dev->gemm_attr_set[slot]) {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
         cudaSuccess)
       return BITLINEAR_ERR_CUDA;
-    dev->gemm_attr_set[1] = true;
+    dev->gemm_attr_set[slot] = true;
   }
   const int pairs = p.total_tiles < dev->sms / 2 ? p.total_tiles : dev->sms / 2;
   if (launch_pdl(kernel, 2 * pairs, bl::kGemmThreads, smem, s, p) != cudaSuccess)
@@ -42,11 +49,12 @@ bitlinear_status launch_pair(const bl::GemmParams& p, DeviceInfo* dev, cudaStrea
   return launch_status();
 }
 
-template <int BN>
-bitlinear_status launch_small(const bl::GemmParams& p, DeviceInfo* dev, int slot,
-                              cudaStream_t s) {
-  auto kernel = bl::gemm_small_kernel<BN>;
-  const int smem = static_cast<int>(sizeof(bl::SmallSmem<BN>)) + 1024;
+template <int BN, class P>
+bitlinear_status launch_small(const P& p, DeviceInfo* dev, int variant, cudaStream_t s) {
+  const int slot = attr_slot<P>(variant);
+  auto kernel = bl::gemm_small_kernel<BN, P>;
+  using Smem = std::conditional_t<P::kEpilogue, bl::SmallEpSmem<BN>, bl::SmallSmem<BN>>;
+  const int smem = static_cast<int>(sizeof(Smem)) + 1024;
   if (!dev->gemm_attr_set[slot]) {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
         cudaSuccess)
@@ -59,10 +67,8 @@ bitlinear_status launch_small(const bl::GemmParams& p, DeviceInfo* dev, int slot
   return launch_status();
 }
 
-}  // namespace
-
-bitlinear_status launch_gemm(int variant, const bl::GemmParams& p, DeviceInfo* dev,
-                             cudaStream_t s) {
+template <class P>
+bitlinear_status launch_variant(int variant, const P& p, DeviceInfo* dev, cudaStream_t s) {
   switch (variant) {
     case 0: return launch_single<128, 7>(p, dev, 0, s);
     case 1: return launch_pair<5>(p, dev, s);
@@ -71,6 +77,18 @@ bitlinear_status launch_gemm(int variant, const bl::GemmParams& p, DeviceInfo* d
     case 5: return launch_small<32>(p, dev, 5, s);
     default: return BITLINEAR_ERR_UNSUPPORTED_SHAPE;
   }
+}
+
+}  // namespace
+
+bitlinear_status launch_gemm(int variant, const bl::GemmParams& p, DeviceInfo* dev,
+                             cudaStream_t s) {
+  return launch_variant(variant, p, dev, s);
+}
+
+bitlinear_status launch_gemm_ep(int variant, const bl::GemmEpParams& p, DeviceInfo* dev,
+                                cudaStream_t s) {
+  return launch_variant(variant, p, dev, s);
 }
 
 cudaError_t device_error_gemm(unsigned int* v, bool clear) {

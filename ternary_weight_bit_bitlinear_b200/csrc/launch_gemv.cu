@@ -7,11 +7,12 @@
 namespace blh {
 namespace {
 
-template <int NT>
-bitlinear_status launch_gemv_tile(const bl::GemvParams& p, DeviceInfo* dev, cudaStream_t s) {
-  auto kernel = bl::gemv_tile_kernel<NT>;
+// per_sm, split_attr_set: this instantiation's once-per-device facts.
+template <int NT, class P>
+bitlinear_status launch_gemv_tile(const P& p, int& per_sm, bool& split_attr_set,
+                                  DeviceInfo* dev, cudaStream_t s) {
+  auto kernel = bl::gemv_tile_kernel<NT, P>;
   constexpr int smem = bl::GemvCfg<NT>::kSmemBytes;
-  int& per_sm = dev->gemv_blocks_per_sm[NT];
   if (per_sm == 0) {
     int nb = 0;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
@@ -32,12 +33,12 @@ bitlinear_status launch_gemv_tile(const bl::GemvParams& p, DeviceInfo* dev, cuda
   const int64_t cap = static_cast<int64_t>(dev->sms) * per_sm * bl::kGemvWarps;
   const int64_t upw = (p.total_units + cap - 1) / cap;
   if (p.total_units < cap || p.total_units * 4 < upw * cap * 3) {
-    auto split = bl::gemv_split_kernel<NT>;
-    if (!dev->gemv_split_attr_set[NT]) {
+    auto split = bl::gemv_split_kernel<NT, P>;
+    if (!split_attr_set) {
       if (cudaFuncSetAttribute(split, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
           cudaSuccess)
         return BITLINEAR_ERR_CUDA;
-      dev->gemv_split_attr_set[NT] = true;
+      split_attr_set = true;
     }
     if (launch_pdl(split, p.total_units, bl::kGemvThreads, smem, s, p) != cudaSuccess)
       return BITLINEAR_ERR_CUDA;
@@ -55,7 +56,9 @@ bitlinear_status launch_gemv_tile(const bl::GemvParams& p, DeviceInfo* dev, cuda
 bitlinear_status launch_gemv(int N, const bl::GemvParams& p, DeviceInfo* dev, cudaStream_t s) {
   switch (N) {
 #define BL_GEMV_CASE(n) \
-  case n: return launch_gemv_tile<n>(p, dev, s);
+  case n:                                                                          \
+    return launch_gemv_tile<n>(p, dev->gemv_blocks_per_sm[n], dev->gemv_split_attr_set[n], \
+                               dev, s);
     BL_GEMV_CASE(1) BL_GEMV_CASE(2) BL_GEMV_CASE(3) BL_GEMV_CASE(4)
     BL_GEMV_CASE(5) BL_GEMV_CASE(6) BL_GEMV_CASE(7) BL_GEMV_CASE(8)
     BL_GEMV_CASE(9) BL_GEMV_CASE(10) BL_GEMV_CASE(11) BL_GEMV_CASE(12)
@@ -63,6 +66,10 @@ bitlinear_status launch_gemv(int N, const bl::GemvParams& p, DeviceInfo* dev, cu
 #undef BL_GEMV_CASE
     default: return BITLINEAR_ERR_UNSUPPORTED_SHAPE;
   }
+}
+
+bitlinear_status launch_gemv_ep(const bl::GemvEpParams& p, DeviceInfo* dev, cudaStream_t s) {
+  return launch_gemv_tile<1>(p, dev->gemv_ep_blocks_per_sm, dev->gemv_ep_split_attr_set, dev, s);
 }
 
 cudaError_t device_error_gemv(unsigned int* v, bool clear) {
