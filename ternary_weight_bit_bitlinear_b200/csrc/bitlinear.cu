@@ -225,7 +225,10 @@ void build_gemm_schedule(bl::GemmParams& p, int sms) {
 }
 
 bl::Epilogue epilogue_of(const bitlinear_linear_problem& q) {
-  return {q.bias, q.residual, q.y, q.ldr, q.ldy, q.dtype, q.activation};
+  const int64_t e = elem_bytes(q.dtype);
+  const bool vec = aligned16(q.y) && aligned16(q.residual) && aligned16(q.bias) &&
+                   q.ldy * e % 16 == 0 && (!q.residual || q.ldr * e % 16 == 0);
+  return {q.bias, q.residual, q.y, q.ldr, q.ldy, q.dtype, q.activation, vec ? 1 : 0};
 }
 
 // Tensor-core GEMM over problems that share N (all validated): one
@@ -234,8 +237,8 @@ bl::Epilogue epilogue_of(const bitlinear_linear_problem& q) {
 // wave.  Ragged edges come from the tensor maps: loads past M, K or N read
 // zeros, and stores past M or N are dropped.  A y whose row pitch (4M bytes)
 // is not a multiple of 16 cannot be a TMA tensor; its epilogue stores directly.
-// `lin`: the epilogues of the same problems (bitlinear_linear), whose outputs
-// take no tensor map; null otherwise.
+// `lin`: the epilogues of the same problems (bitlinear_linear, N > 128), whose
+// outputs take no tensor map; null otherwise.
 template <class Params>
 bitlinear_status gemm_group(const bitlinear_problem* probs, int64_t count, int64_t N,
                             cudaStream_t s, const bitlinear_linear_problem* lin = nullptr) {
@@ -269,7 +272,7 @@ bitlinear_status gemm_group(const bitlinear_problem* probs, int64_t count, int64
     int64_t tiles = 0;
     for (int i = 0; i < n; ++i) {
       const bitlinear_problem& q = probs[base + order[i]];
-      // the small kernel and the epilogues store directly
+      // the small kernel and the epilogue store directly
       const bool direct = small || Params::kEpilogue || q.M % 4 != 0;
       // packed weights: one k-block (32 bytes) per row, or for the small kernel
       // four k-blocks (128 bytes, swizzled) per row
@@ -303,11 +306,10 @@ bitlinear_status gemm_group(const bitlinear_problem* probs, int64_t count, int64
     p.total_tiles = static_cast<int>(tiles);
     p.wait_ns = blh::wait_limit_ns();
     build_gemm_schedule(p, wide ? dev->sms / 2 : dev->sms);
-    const int variant = small ? (BN == 16 ? 4 : 5) : wide ? 1 : BN == 64 ? 3 : 0;
-    if constexpr (Params::kEpilogue)
-      st = blh::launch_gemm_ep(variant, p, dev, s);
+    if constexpr (Params::kEpilogue)   // N > 128
+      st = blh::launch_pair_ep(p, dev, s);
     else
-      st = blh::launch_gemm(variant, p, dev, s);
+      st = blh::launch_gemm(small ? (BN == 16 ? 4 : 5) : wide ? 1 : BN == 64 ? 3 : 0, p, dev, s);
     if (st != BITLINEAR_OK) return st;
   }
   return BITLINEAR_OK;
@@ -337,19 +339,129 @@ bitlinear_problem product_of(const bitlinear_linear_problem& q) {
   return {q.packed, q.alpha, q.M, q.K, q.xq, q.amax, q.xsum, nullptr, nullptr};
 }
 
-// Validated problems sharing N.  One token takes the GEMV (one launch per
-// kGemvEpMaxProblems problems), more the tensor cores.
+// The cluster-split GEMM over up to kGemmMaxProblems problems, each of at
+// least S stages (every pair of a cluster needs one).
+bitlinear_status linear_split(const bitlinear_linear_problem* probs, int n, int64_t N, int BN,
+                              int S, DeviceInfo* dev, cudaStream_t s) {
+  bl::SplitParams p;
+  const int G = bl::split_stage_kb(BN);
+  const int64_t n_tiles = (N + BN - 1) / BN;
+  int64_t tiles = 0;
+  for (int i = 0; i < n; ++i) {
+    const bitlinear_linear_problem& q = probs[i];
+    if (!encode_u8_2d(&p.tmA[i], q.packed, static_cast<uint64_t>(packed_row_words(q.K) * 4),
+                      static_cast<uint64_t>(q.M), G * bl::kGemmPackedRowBytes, bl::kGemmBM,
+                      G == 4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B) ||
+        !encode_u8_2d(&p.tmB[i], q.xq, static_cast<uint64_t>(q.K), static_cast<uint64_t>(N),
+                      bl::kGemmBK, BN / 2, CU_TENSOR_MAP_SWIZZLE_128B))
+      return BITLINEAR_ERR_CUDA;
+    p.prob[i] = {q.alpha, q.amax, q.xsum, nullptr, nullptr,
+                 static_cast<int>(q.M), static_cast<int>(q.K), static_cast<int>(N),
+                 static_cast<int>(n_tiles), static_cast<int>(tiles), 1};
+    p.ep[i] = epilogue_of(q);
+    tiles += (q.M + bl::kPairBM - 1) / bl::kPairBM * n_tiles;
+    if (tiles > INT_MAX) return BITLINEAR_ERR_UNSUPPORTED_SHAPE;
+  }
+  p.num_problems = n;
+  p.total_tiles = static_cast<int>(tiles);
+  p.wait_ns = blh::wait_limit_ns();
+  return blh::launch_split(BN, S, p, dev, s);
+}
+
+// How bitlinear_linear runs up to kGemmMaxProblems problems of N tokens on the
+// tensor cores: BN tokens per tile and S CTA pairs per cluster, or BN = 256
+// for the kernel of gemm_pair.cuh.  The shortest estimate in ns wins.
+//
+// What the estimates are made of, measured on B200 (cycles at 1.9 GHz): a
+// k-block of a 256-row tile takes 106 ns at up to 64 tokens, 156 at 128 (the
+// MMAs alone 135) and 323 in the BN = 256 kernel; the exchange of partial sums
+// costs 700 + 10 BN ns with two pairs and 1400 + 12 BN with four; a warp
+// finishes a block of 16 tokens in 740 ns, or 960 while the next tile's weights
+// are expanded beside it, and three warps share the last tile's blocks.
+// For instance (us; estimate without the launch, measured in the order of S):
+//   2560 x 2560, 128 tokens:  9.3 / 9.0 / 8.2 for S = 1 / 2 / 4
+//   8192 x 28672, 16 tokens: 28.4 / 18.7 / 24.3;  128 tokens: 43.4 / 27.8 / 37.0
+//   11008 x 4096, 16 tokens:  8.3 / 10.0 / 11.8 (43 tiles fit in no two rounds)
+//   11008 x 4096, 512 tokens: 30.0 at BN = 128, 33.9 at 256; 2048: 94.8 and 72.3
+struct LinearPlan {
+  int BN = 0, S = 1;
+  int64_t cost = INT64_MAX;
+};
+
+bitlinear_status plan_linear(const bitlinear_linear_problem* probs, int n, int64_t N,
+                             DeviceInfo* dev, LinearPlan* best) {
+  auto shape = [&](int BN, int G, int64_t* tiles, int64_t* kb, int64_t* stages) {
+    int64_t sum = 0;
+    *tiles = 0;
+    *stages = INT64_MAX;
+    for (int i = 0; i < n; ++i) {
+      const int64_t k = (probs[i].K + bl::kGemmBK - 1) / bl::kGemmBK;
+      const int64_t t = (probs[i].M + bl::kPairBM - 1) / bl::kPairBM * ((N + BN - 1) / BN);
+      *tiles += t;
+      sum += t * k;
+      *stages = std::min(*stages, (k + G - 1) / G);
+    }
+    *kb = (sum + *tiles - 1) / *tiles;
+  };
+  int64_t tiles, kb, stages;
+  for (int BN = 32; BN <= 128; BN *= 2) {
+    if (BN > 32 && N <= BN / 2) break;
+    shape(BN, bl::split_stage_kb(BN), &tiles, &kb, &stages);
+    for (int S = 1; S <= bl::kSplitMaxPairs && S <= stages; S *= 2) {
+      int clusters = 0;
+      const bitlinear_status st = blh::split_clusters(BN, S, dev, &clusters);
+      if (st != BITLINEAR_OK) return st;
+      const int64_t rounds = (tiles + clusters - 1) / clusters, own = BN / S;
+      int64_t round = (kb + S - 1) / S * (BN == 128 ? 156 : 106);
+      if (S > 1) round += S == 2 ? 700 + 10 * BN : 1400 + 12 * BN;
+      if (rounds > 1) round = std::max<int64_t>(round, (own + 15) / 16 * 960);
+      const int64_t cost = rounds * round + (own + 47) / 48 * 740 + 3500;
+      if (cost < best->cost) *best = {BN, S, cost};
+    }
+  }
+  if (N > 128) {
+    shape(bl::kPairBN, 1, &tiles, &kb, &stages);
+    const int64_t pairs = dev->sms / 2;
+    const int64_t cost = (tiles + pairs - 1) / pairs * kb * 323 + 10000;
+    if (cost < best->cost) *best = {bl::kPairBN, 1, cost};
+  }
+  return BITLINEAR_OK;
+}
+
+// Whether N tokens run on the CUDA cores: always up to two, up to eight while
+// the products are small (2560 x 2560 at 3 / 4 / 8 tokens: 3.5 / 4.0 / 6.9 us
+// against 6.0 on the tensor cores; 11008 x 4096 at 2 / 4: 6.9 / 8.4 against
+// 8.1; 8192 x 28672 at 2 / 3: 15.8 / 21.3 against 18.4).
+bool linear_on_cuda_cores(const bitlinear_linear_problem* probs, int64_t count, int64_t N) {
+  if (N <= 2) return true;
+  if (N > bl::kGemvEpMaxTokens) return false;
+  int64_t weights = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    weights += probs[i].M * probs[i].K;
+    if (N * weights > int64_t(32) << 20) return false;
+  }
+  return true;
+}
+
+// Validated problems sharing N.
 bitlinear_status linear_group(const bitlinear_linear_problem* probs, int64_t count, int64_t N,
                               cudaStream_t s) {
   DeviceInfo* dev = nullptr;
   bitlinear_status st = device_info(&dev);
   if (st != BITLINEAR_OK) return st;
-  if (N > 1) {
-    bitlinear_problem products[bl::kGemmMaxProblems];
+  if (!linear_on_cuda_cores(probs, count, N)) {
     for (int64_t base = 0; base < count; base += bl::kGemmMaxProblems) {
-      const int64_t n = std::min<int64_t>(count - base, bl::kGemmMaxProblems);
-      for (int64_t i = 0; i < n; ++i) products[i] = product_of(probs[base + i]);
-      st = gemm_group<bl::GemmEpParams>(products, n, N, s, probs + base);
+      const bitlinear_linear_problem* q = probs + base;
+      const int n = static_cast<int>(std::min<int64_t>(count - base, bl::kGemmMaxProblems));
+      LinearPlan plan;
+      if ((st = plan_linear(q, n, N, dev, &plan)) != BITLINEAR_OK) return st;
+      if (plan.BN == bl::kPairBN) {
+        bitlinear_problem products[bl::kGemmMaxProblems];
+        for (int i = 0; i < n; ++i) products[i] = product_of(q[i]);
+        st = gemm_group<bl::GemmEpParams>(products, n, N, s, q);
+      } else {
+        st = linear_split(q, n, N, plan.BN, plan.S, dev, s);
+      }
       if (st != BITLINEAR_OK) return st;
     }
     return BITLINEAR_OK;
@@ -367,7 +479,7 @@ bitlinear_status linear_group(const bitlinear_linear_problem* probs, int64_t cou
     }
     p.num_problems = n;
     p.total_units = static_cast<int>(units);
-    if ((st = blh::launch_gemv_ep(p, dev, s)) != BITLINEAR_OK) return st;
+    if ((st = blh::launch_gemv_ep(static_cast<int>(N), p, dev, s)) != BITLINEAR_OK) return st;
   }
   return BITLINEAR_OK;
 }

@@ -90,4 +90,43 @@ __device__ __forceinline__ float activate(float v, int act) {
   }
 }
 
+// act(v) behind a product, where nothing is rounded to codes: the divisions of
+// silu and of gelu_tanh (in its form v / (1 + e^-2a), a the argument of tanh)
+// are approximate, within 2 units in the last place.  The exponential's
+// argument stops at 87 (the approximate division wants a divisor below 2^126):
+// at most |v| 2^-125 is added by that.  Of a 2560 x 2560 product of 256 tokens
+// silu takes 2.1 us with exact divisions, 1.2 with these.
+__device__ __forceinline__ float activate_product(float v, int act) {
+  if (act == BITLINEAR_ACT_SILU) {
+    const float a = v < -87.0f ? -87.0f : v;
+    return __fdividef(v, __fadd_rn(1.0f, expf(-a)));
+  }
+  if (act == BITLINEAR_ACT_GELU_TANH) {
+    const float c = __fmul_rn(__fmul_rn(__fmul_rn(0.044715f, v), v), v);
+    const float t = __fmul_rn(2.0f * 0.7978845608028654f, __fadd_rn(v, c));
+    const float a = t < -87.0f ? -87.0f : t;
+    return __fdividef(v, __fadd_rn(1.0f, expf(-a)));
+  }
+  return activate(v, act);
+}
+
+// activate_product over n values, the choice made once.
+template <int n>
+__device__ __forceinline__ void activate_all(float (&f)[n], int act) {
+  switch (act) {
+#define BL_ACT_ALL(a)                                                               \
+  case a: {                                                                         \
+    _Pragma("unroll") for (int i = 0; i < n; ++i) f[i] = activate_product(f[i], a); \
+    break;                                                                          \
+  }
+    BL_ACT_ALL(BITLINEAR_ACT_RELU)
+    BL_ACT_ALL(BITLINEAR_ACT_RELU2)
+    BL_ACT_ALL(BITLINEAR_ACT_SILU)
+    BL_ACT_ALL(BITLINEAR_ACT_GELU)
+    BL_ACT_ALL(BITLINEAR_ACT_GELU_TANH)
+#undef BL_ACT_ALL
+    default: break;
+  }
+}
+
 }  // namespace bl

@@ -127,18 +127,46 @@ struct GemmSmem {
   int abort;
 };
 
-// Epilogue of one 32-token x 32-row block (r: this lane's row m, tokens n0
-// ..): the rescaled accumulators go through this warp's staging block so that
-// the rest runs as a loop over tokens (each lane reads back what it wrote).
-__device__ __forceinline__ void gemm_ep_block(const Epilogue& ep, const uint32_t (&r)[32],
-                                              const int* xs, const float* sc, float* blk, int n0,
-                                              int N, int m, int M, int lane) {
+// The epilogue of bitlinear_linear over this warp's 32-token chunks (half,
+// half + 2, ...) of a tile of BN tokens, for its 32 weight rows from m0, in
+// blocks of 16 tokens.  `wait` waits for the accumulator (false: given up),
+// `chunk` reads 16 columns of it from a column.  The first residual is on its
+// way before the wait.
+template <int BN, class Wait, class Chunk>
+__device__ __forceinline__ bool gemm_epilogue(const Epilogue& ep, int n_tile, int N, int m0, int M,
+                                              int half, int lane, const int* xs, const float* sc,
+                                              float* blk, Wait&& wait, Chunk&& chunk) {
+  bool ok = true;
+  ep_dispatch(ep.dtype, [&](auto type) {
+    EpRows<decltype(type), 16> rows;
+    rows.begin(ep, m0, M, lane);
+    rows.load(ep, n_tile + half * 32, m0 < M ? N : 0, rows.res);
+    if (!wait()) {
+      ok = false;
+      return;
+    }
+    int col = half * 32;                   // of the tile: 16 columns, then the chunk's other 16
+#pragma unroll 1
+    for (int i = 0; col < BN; ++i) {
+      const int n0 = n_tile + col;
+      if (n0 >= N || m0 >= M) break;       // nothing to store from here on
+      uint32_t r[16];
+      chunk(col, r);
+      __syncwarp();                        // the block's last values have been read
 #pragma unroll
-  for (int j = 0; j < 32; ++j)
-    blk[j * 32 + lane] = __fmul_rn(__int2float_rn(static_cast<int>(r[j]) - xs[j]), sc[j]);
-  if (m >= M) return;
-#pragma unroll 4
-  for (int j = 0; j < min(32, N - n0); ++j) ep_element(ep, n0 + j, m, blk[j * 32 + lane]);
+      for (int j = 0; j < 16; ++j)         // this lane's row of 16 tokens, rescaled
+        blk[j * 32 + lane] =
+            __fmul_rn(__int2float_rn(static_cast<int>(r[j]) - xs[i * 16 + j]), sc[i * 16 + j]);
+      __syncwarp();
+      col += i & 1 ? 48 : 16;
+      uint4 next[decltype(rows)::kIters] = {};
+      if (col < BN) rows.load(ep, n_tile + col, N, next);
+      rows.finish(ep, blk, n0, N, M);
+#pragma unroll
+      for (int q = 0; q < decltype(rows)::kIters; ++q) rows.res[q] = next[q];
+    }
+  });
+  return ok;
 }
 
 // Before the CTA releases its shared memory: wait for the TMA loads still in
@@ -153,8 +181,8 @@ __device__ __forceinline__ void gemm_drain_loads(uint64_t* full, int issued) {
     mbar_drain(&full[i % STAGES], static_cast<uint32_t>((i / STAGES) & 1));
 }
 
-template <int BN>
-__device__ __forceinline__ void gemm_locate(const GemmParams& p, int tile, int& pi, int& m_blk,
+template <int BN, class P>
+__device__ __forceinline__ void gemm_locate(const P& p, int tile, int& pi, int& m_blk,
                                             int& n_blk) {
   pi = 0;
   while (pi + 1 < p.num_problems && tile >= p.prob[pi + 1].tile_begin) ++pi;
@@ -185,9 +213,9 @@ __device__ __forceinline__ void gemm_tile_at(const GemmParams& p, int i, int& pi
                    n_blk);
 }
 
-template <int BN, int STAGES, class P>
+template <int BN, int STAGES>
 __global__ void __launch_bounds__(kGemmThreads, 1)
-gemm_i8_tcgen05_kernel(const __grid_constant__ P p) {
+gemm_i8_tcgen05_kernel(const __grid_constant__ GemmParams p) {
   extern __shared__ uint8_t smem_raw[];
   using Smem = GemmSmem<BN, STAGES>;
   const uint32_t base = smem_u32(smem_raw);
@@ -399,11 +427,6 @@ gemm_i8_tcgen05_kernel(const __grid_constant__ P p) {
         tmem_ld_wait();
         const int n0 = n_blk * BN + cc * 32;
         if (n0 >= pr.N) continue;          // tokens past N: nothing to store
-        if constexpr (P::kEpilogue) {
-          gemm_ep_block(p.ep[pi], r, xs + (cc >> 1) * 32, sc + (cc >> 1) * 32, s.ep_out[e], n0,
-                        pr.N, m, pr.M, lane);
-          continue;
-        }
         if (pr.direct_store) {   // rows past M and tokens past N are not stored
 #pragma unroll
           for (int j = 0; j < 32; ++j) {

@@ -256,8 +256,14 @@ gemm_i8_pair_kernel(const __grid_constant__ P p) {
       gemm_tile_at<kPairBN>(p, pair, npairs, ti, pi, m_blk, n_blk);
       const GemmProblem pr = p.prob[pi];   // by value: registers, not parameter-space reloads
       const uint32_t ab = it & 1, ap = (it >> 1) & 1;
-      if (!mbar_wait_cluster_warp(&s.tfull[ab], ap, abort, p.wait_ns)) break;
-      tc_fence_after();
+      auto wait = [&]() {
+        const bool ok = mbar_wait_cluster_warp(&s.tfull[ab], ap, abort, p.wait_ns);
+        tc_fence_after();
+        return ok;
+      };
+      if constexpr (!P::kEpilogue) {
+        if (!wait()) break;
+      }
       const int m_base = m_blk * kPairBM + static_cast<int>(rank) * kGemmBM;
       const int m = m_base + r_in_tile;
       float* sc = s.ep_scale[e];
@@ -280,6 +286,16 @@ gemm_i8_pair_kernel(const __grid_constant__ P p) {
         }
         __syncwarp();
       }
+      if constexpr (P::kEpilogue) {
+        if (!gemm_epilogue<kPairBN>(
+                p.ep[pi], n_blk * kPairBN, pr.N, m_base + static_cast<int>(quarter) * 32, pr.M,
+                half, lane, xs, sc, s.ep_out[e], wait, [&](int col, uint32_t (&r)[16]) {
+                  tmem_ld_32x32b_x16(
+                      tmem_base + ((quarter * 32u) << 16) + ab * kPairBN + col, r);
+                  tmem_ld_wait();
+                }))
+          break;
+      } else {
 #pragma unroll 1
       for (int cc = half; cc < kPairBN / 32; cc += 2) {
         uint32_t r[32];
@@ -288,11 +304,6 @@ gemm_i8_pair_kernel(const __grid_constant__ P p) {
         tmem_ld_wait();
         const int n0 = n_blk * kPairBN + cc * 32;
         if (n0 >= pr.N) continue;          // tokens past N: nothing to store
-        if constexpr (P::kEpilogue) {
-          gemm_ep_block(p.ep[pi], r, xs + (cc >> 1) * 32, sc + (cc >> 1) * 32, s.ep_out[e], n0,
-                        pr.N, m, pr.M, lane);
-          continue;
-        }
         if (pr.direct_store) {   // rows past M and tokens past N are not stored
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
@@ -322,6 +333,7 @@ gemm_i8_pair_kernel(const __grid_constant__ P p) {
           tma_store_2d(&p.tmY[pi], blk, m_base + static_cast<int>(quarter) * 32, n0);
           bulk_commit_group();
         }
+      }
       }
       tc_fence_before();
       __syncwarp();

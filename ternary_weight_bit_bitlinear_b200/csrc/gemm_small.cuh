@@ -50,8 +50,6 @@
 // and MMAs it has issued before it releases tensor memory.
 #pragma once
 
-#include <type_traits>
-
 #include "gemm.cuh"
 
 namespace bl {
@@ -86,16 +84,9 @@ struct SmallSmem {
   uint32_t tmem_slot;
   int abort;
 };
-// With an epilogue: a staging block per epilogue warp, [token][row].
-template <int BN>
-struct SmallEpSmem : SmallSmem<BN> {
-  float ep_out[4][BN * 32];
-};
 static_assert(small_aslots(16) == 3 && small_aslots(32) == 3, "three A slots");
 static_assert(sizeof(SmallSmem<16>) + 1024 <= 232448, "shared memory");
 static_assert(sizeof(SmallSmem<32>) + 1024 <= 232448, "shared memory");
-static_assert(sizeof(SmallEpSmem<16>) + 1024 <= 232448, "shared memory");
-static_assert(sizeof(SmallEpSmem<32>) + 1024 <= 232448, "shared memory");
 
 // Ring position of a k-group: its stage's k-groups get consecutive sequence
 // numbers, and sequence number q uses A slot q % kSlots.
@@ -107,11 +98,11 @@ struct SmallSlot {
   }
 };
 
-template <int BN, class P>
+template <int BN>
 __global__ void __launch_bounds__(kSmallThreads, 1)
-gemm_small_kernel(const __grid_constant__ P p) {
+gemm_small_kernel(const __grid_constant__ GemmParams p) {
   extern __shared__ uint8_t smem_raw[];
-  using Smem = std::conditional_t<P::kEpilogue, SmallEpSmem<BN>, SmallSmem<BN>>;
+  using Smem = SmallSmem<BN>;
   constexpr int S = Smem::S;
   constexpr int kSlots = small_aslots(BN);
   constexpr uint32_t kAColBase = small_acol_base(BN);
@@ -356,32 +347,16 @@ gemm_small_kernel(const __grid_constant__ P p) {
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.tempty[db]);
       const int m = m_blk * kGemmBM + static_cast<int>(quarter) * 32 + lane;
-      if constexpr (P::kEpilogue) {
-        float* blk = s.ep_out[quarter];
 #pragma unroll
-        for (int j = 0; j < BN; ++j) {
-          const float scj = __shfl_sync(0xFFFFFFFFu, sc, j);
-          const int xsj = __shfl_sync(0xFFFFFFFFu, xs, j);
-          blk[j * 32 + lane] = __fmul_rn(__int2float_rn(static_cast<int>(r[j]) - xsj), scj);
-        }
-        if (m < pr.M) {   // each lane reads back what it wrote
-          const int n0 = n_blk * BN;
-#pragma unroll 4
-          for (int j = 0; j < min(BN, pr.N - n0); ++j)
-            ep_element(p.ep[pi], n0 + j, m, blk[j * 32 + lane]);
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < BN; ++j) {
-          const float scj = __shfl_sync(0xFFFFFFFFu, sc, j);
-          const int xsj = __shfl_sync(0xFFFFFFFFu, xs, j);
-          const int n = n_blk * BN + j;
-          if (n < pr.N && m < pr.M) {
-            const int a = static_cast<int>(r[j]) - xsj;
-            const int64_t o = static_cast<int64_t>(n) * pr.M + m;
-            pr.y[o] = __fmul_rn(__int2float_rn(a), scj);
-            if (pr.acc) pr.acc[o] = a;
-          }
+      for (int j = 0; j < BN; ++j) {
+        const float scj = __shfl_sync(0xFFFFFFFFu, sc, j);
+        const int xsj = __shfl_sync(0xFFFFFFFFu, xs, j);
+        const int n = n_blk * BN + j;
+        if (n < pr.N && m < pr.M) {
+          const int a = static_cast<int>(r[j]) - xsj;
+          const int64_t o = static_cast<int64_t>(n) * pr.M + m;
+          pr.y[o] = __fmul_rn(__int2float_rn(a), scj);
+          if (pr.acc) pr.acc[o] = a;
         }
       }
     }

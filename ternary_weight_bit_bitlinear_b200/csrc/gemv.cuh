@@ -38,6 +38,7 @@ constexpr int kGemvThreads = kGemvWarps * 32;
 constexpr int kGemvMaxTokens = 16;
 constexpr int kGemvMaxProblems = 256;
 constexpr int kGemvEpMaxProblems = 64;
+constexpr int kGemvEpMaxTokens = 8;
 
 template <int NT>
 struct GemvCfg {

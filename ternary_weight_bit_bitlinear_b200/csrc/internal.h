@@ -16,6 +16,7 @@
 #include "bitlinear.h"
 #include "gemm.cuh"
 #include "gemm_pair.cuh"
+#include "gemm_split.cuh"
 #include "gemv.cuh"
 #include "gemv_quant.cuh"
 #include "norm.cuh"
@@ -28,7 +29,7 @@ constexpr int kMaxDevices = 64;
 // Per-device facts and one-time set-up flags, looked up once per device.
 struct DeviceInfo {
   int sms = 0;
-  bool gemm_attr_set[16] = {};
+  bool gemm_attr_set[8] = {};
   int gemv_blocks_per_sm[bl::kGemvMaxTokens + 1] = {};   // 0: not set up yet
   int tl2_blocks_per_sm[bl::kGemvMaxTokens + 1] = {};    // 0: not set up yet
   bool gq_attr_set[bl::kGemvMaxTokens + 1] = {};
@@ -36,8 +37,10 @@ struct DeviceInfo {
   int gq_area[bl::kGemvMaxTokens + 1][bl::kGqMaxWarps + 1] = {};   // last shared-memory size
   int gq_occ[bl::kGemvMaxTokens + 1][bl::kGqMaxWarps + 1] = {};    // and its CTAs per SM
   bool gemv_split_attr_set[bl::kGemvMaxTokens + 1] = {};
-  int gemv_ep_blocks_per_sm = 0;      // 0: not set up yet
-  bool gemv_ep_split_attr_set = false;
+  int gemv_ep_blocks_per_sm[bl::kGemvEpMaxTokens + 1] = {};     // 0: not set up yet
+  bool gemv_ep_split_attr_set[bl::kGemvEpMaxTokens + 1] = {};
+  bool split_attr_set[3] = {};        // gemm_split_kernel: 32, 64, 128 tokens
+  int split_clusters[3][3] = {};      // resident clusters of 1, 2, 4 pairs; 0: not asked yet
 };
 
 // The calling thread's current device.
@@ -72,8 +75,10 @@ inline bitlinear_status launch_status() {
 // launch_gemv.cu: decode GEMV on int8 activations (tile or split-unit kernel).
 bitlinear_status launch_gemv(int N, const bl::GemvParams& p, DeviceInfo* dev, cudaStream_t s);
 
-// The one-token launch of bitlinear_linear (same kernels, with the epilogue).
-bitlinear_status launch_gemv_ep(const bl::GemvEpParams& p, DeviceInfo* dev, cudaStream_t s);
+// The few-token launch of bitlinear_linear (same kernels, with the epilogue),
+// N <= kGemvEpMaxTokens.
+bitlinear_status launch_gemv_ep(int N, const bl::GemvEpParams& p, DeviceInfo* dev,
+                                cudaStream_t s);
 
 // launch_norm.cu: row operators between two products, one CTA per row.
 bitlinear_status launch_norm(bool gated, int rows, int dtype, const bl::NormParams& p,
@@ -91,8 +96,14 @@ bitlinear_status gemv_quant_launch(int N, int grid, int warps, const bl::GqParam
 bitlinear_status launch_gemm(int variant, const bl::GemmParams& p, DeviceInfo* dev,
                              cudaStream_t s);
 
-bitlinear_status launch_gemm_ep(int variant, const bl::GemmEpParams& p, DeviceInfo* dev,
-                                cudaStream_t s);
+// The CTA-pair GEMM with an epilogue (bitlinear_linear, many tokens).
+bitlinear_status launch_pair_ep(const bl::GemmEpParams& p, DeviceInfo* dev, cudaStream_t s);
+
+// The cluster-split GEMM of bitlinear_linear, BN tokens per tile, S CTA pairs
+// per cluster; split_clusters: how many such clusters the device holds at once.
+bitlinear_status launch_split(int BN, int S, const bl::SplitParams& p, DeviceInfo* dev,
+                              cudaStream_t s);
+bitlinear_status split_clusters(int BN, int S, DeviceInfo* dev, int* out);
 
 // launch_tl2.cu: TL2-style storage.
 bitlinear_status launch_gemv_tl2(int N, const bl::Tl2Params& p, DeviceInfo* dev,

@@ -68,8 +68,18 @@ bitlinear_status launch_gemv(int N, const bl::GemvParams& p, DeviceInfo* dev, cu
   }
 }
 
-bitlinear_status launch_gemv_ep(const bl::GemvEpParams& p, DeviceInfo* dev, cudaStream_t s) {
-  return launch_gemv_tile<1>(p, dev->gemv_ep_blocks_per_sm, dev->gemv_ep_split_attr_set, dev, s);
+bitlinear_status launch_gemv_ep(int N, const bl::GemvEpParams& p, DeviceInfo* dev,
+                                cudaStream_t s) {
+  switch (N) {
+#define BL_GEMV_EP_CASE(n)                                       \
+  case n:                                                        \
+    return launch_gemv_tile<n>(p, dev->gemv_ep_blocks_per_sm[n], \
+                               dev->gemv_ep_split_attr_set[n], dev, s);
+    BL_GEMV_EP_CASE(1) BL_GEMV_EP_CASE(2) BL_GEMV_EP_CASE(3) BL_GEMV_EP_CASE(4)
+    BL_GEMV_EP_CASE(5) BL_GEMV_EP_CASE(6) BL_GEMV_EP_CASE(7) BL_GEMV_EP_CASE(8)
+#undef BL_GEMV_EP_CASE
+    default: return BITLINEAR_ERR_UNSUPPORTED_SHAPE;
+  }
 }
 
 cudaError_t device_error_gemv(unsigned int* v, bool clear) {

@@ -92,7 +92,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   unsigned long long t0 = global_timer_ns();
   for (uint32_t i = 1;; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 15u) == 0) {
+    if ((i & 7u) == 0) {
       if (*abort) return false;
       if (global_timer_ns() - t0 > limit_ns) {
         *abort = 1;
@@ -158,6 +158,14 @@ __device__ __forceinline__ void tma_load_2d(void* smem_dst, const CUtensorMap* m
       " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(smem_dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y)
       : "memory");
+}
+
+// The box of a tiled load into L2 (a hint).
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y)
+               : "memory");
 }
 
 // Untiled bulk copy of `bytes` (a multiple of 16) from global to this CTA's
@@ -377,9 +385,47 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
   return r;
 }
 
+__device__ __forceinline__ uint32_t cluster_nctarank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+
+// Address of this CTA's shared-memory location `p` in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t map_cluster(const void* p, int rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+
+// Asynchronous 16-byte store into CTA `rank` of the cluster, at the offset of
+// `p`; its bytes count on the barrier at `bar`'s offset there, which makes them
+// visible to who waits on it.
+__device__ __forceinline__ void st_async_v4(void* p, uint64_t* bar, int rank, uint32_t a,
+                                            uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile(
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%2, %3, %4, %5}, [%1];"
+      ::"r"(map_cluster(p, rank)),
+      "r"(map_cluster(bar, rank)), "r"(a), "r"(b), "r"(c), "r"(d)
+      : "memory");
+}
+
+// Arrive on the barrier at `bar`'s offset in CTA `rank`.  Orders nothing but
+// this thread's own shared-memory and tensor-memory work (an arrival with
+// cluster-scope release takes about 1000 cycles).
+__device__ __forceinline__ void mbar_arrive_cluster(uint64_t* bar, int rank) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(map_cluster(bar, rank))
+               : "memory");
+}
+
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
                ::: "memory");
+}
+
+// The meeting alone, without ordering memory.
+__device__ __forceinline__ void cluster_sync_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
 // Arrive on the barrier at the same offset in the rank-0 CTA (the default
@@ -412,7 +458,7 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
   unsigned long long t0 = global_timer_ns();
   for (uint32_t i = 1;; ++i) {
     if (mbar_try_wait_cluster(bar, parity)) return true;
-    if ((i & 15u) == 0) {
+    if ((i & 7u) == 0) {
       if (*abort) return false;
       if (global_timer_ns() - t0 > limit_ns) {
         *abort = 1;
@@ -473,6 +519,26 @@ __device__ __forceinline__ void mma_i8_ss_pair(uint32_t d_tmem, uint64_t a_desc,
       : "memory");
 }
 
+// The same with A in tensor memory: 128 rows in each CTA's, at one address.
+__device__ __forceinline__ void mma_i8_ts_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                               uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::i8 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem), "r"(a_tmem),
+      "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Arrive once on the barrier at `bar`'s offset in the CTAs of the cluster that
+// `mask` names when every MMA issued so far by this thread has completed.
+__device__ __forceinline__ void mma_commit_mask(uint64_t* bar, uint16_t mask) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;" ::"r"(smem_u32(bar)), "h"(mask)
+      : "memory");
+}
+
 // Arrive once on the barrier at `bar`'s offset in both CTAs of the pair when
 // every MMA issued so far by this thread has completed.
 __device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
@@ -507,6 +573,11 @@ __host__ __device__ constexpr uint32_t idesc_i8(int M, int N) {
          | (1u << 10)                               // B: signed 8-bit
          | (static_cast<uint32_t>(N >> 3) << 17)    // N / 8
          | (static_cast<uint32_t>(M >> 4) << 24);   // M / 16
+}
+
+// The same with unsigned A.
+__host__ __device__ constexpr uint32_t idesc_u8s8(int M, int N) {
+  return idesc_i8(M, N) & ~(1u << 7);
 }
 
 }  // namespace bl

@@ -71,8 +71,20 @@ def act64(v, name):
 # units of |u| / 2 < 6 |u|.  gelu_tanh: its argument carries 5 roundings
 # (slope: |a tanh'(a)| < 0.45, so < 2.3), tanhf within 2 units (4), the sum
 # (2), two products (4): below 13 |u| / 2 < 7 |u|.
-def act_error(u, name):
+#
+# Behind a product the kernels divide approximately (__fdividef, within 2 units:
+# 4 half steps, instead of 1), and stop the exponential's argument at 87:
+# silu  4 + 1 + 4 = 9 of |y|, plus |v| 2^-125.
+# gelu_tanh as v / (1 + e^-a), a = 2 sqrt(2/pi) (v + 0.044715 v^3) with 5
+# roundings: e^-a is off by 5 |a| + 4, which passes on e^-a / (1 + e^-a) of it;
+# |y| |a| e^-a / (1 + e^-a) <= 0.37 |v| on either side, so 5 * 0.37 + 4 + 1 + 4
+# < 11 of |v|, plus |v| 2^-125.
+def act_error(u, name, product=False):
     au = np.abs(u)
+    if product and name == "silu":
+        return 9 * U * np.abs(act64(u, "silu")) + au * 2.0 ** -125
+    if product and name == "gelu_tanh":
+        return 11 * U * au
     if name in (None, "none", "relu"):
         return np.zeros_like(u)
     if name == "relu2":
@@ -99,7 +111,7 @@ def linear64(acc, alpha, amax, bias, name, residual, dtype):
     if bias is not None:
         err = err + U * np.abs(u)
     y = act64(u, name)
-    err = err * act_slope(u, name) + act_error(u, name)
+    err = err * act_slope(u, name) + act_error(u, name, product=True)
     if residual is not None:
         y = y + residual.astype(np.float64)
         err = err + U * np.abs(y)

@@ -416,3 +416,89 @@ def test_mlp_block_on_another_stream_and_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want2)
+
+
+# ------------------------------------------- every split and round of linear
+
+# Tokens x rows x K chosen so that the tensor-core path runs with one, two and
+# four pairs per cluster, one tile and several per cluster, a last tile of a
+# single token, clusters whose later pairs finish no token, K of one stage.
+SPLITS = [(9, 12800, 16384), (17, 12800, 16384), (33, 11008, 4096), (65, 11008, 4096),
+          (129, 2560, 2560), (200, 6912, 2560), (3, 19000, 4112), (40, 300, 28672),
+          (130, 300, 28672), (16, 40000, 1040), (96, 40000, 1040), (300, 20000, 528),
+          (257, 513, 16400), (64, 8192, 8192), (512, 2560, 6912), (5, 257, 131072),
+          (1000, 1040, 1040), (2048, 640, 2560)]
+
+
+@pytest.mark.parametrize("N,M,K", SPLITS)
+def test_linear_equals_gemm_at_every_split(N, M, K):
+    """The accumulators are integers: whatever the split, the product without
+    an epilogue has the bits of the library's other GEMM."""
+    packed, alpha = api.pack_weights(inputs.latent_weights(M, K, seed=N + M, device="cuda"))
+    q = api.quant_act(inputs.activations(N, K, seed=K, device="cuda", outlier_frac=0.01))
+    want = api.gemm(packed, alpha, *q)
+    for _ in range(2):                              # the second finds warm plans and caches
+        assert torch.equal(api.linear(packed, alpha, *q), want)
+    b, r = torch.randn(M, device="cuda"), rows(N, M, 1, torch.bfloat16)
+    y = api.linear(packed, alpha, *q, bias=b, activation="relu2", residual=r)
+    z = torch.clamp_min(want + b, 0)
+    assert torch.equal(y, (z * z + r.float()).to(torch.bfloat16))
+
+
+def test_linear_equals_gemm_on_drawn_shapes():
+    import random
+    rng = random.Random(7)
+    for i in range(40):
+        N = int(round(2 ** rng.uniform(0, 9.5)))
+        M = int(round(2 ** rng.uniform(0, 13.5)))
+        K = 16 * int(round(2 ** rng.uniform(0, 9.5)))
+        packed, alpha = api.pack_weights(inputs.latent_weights(M, K, seed=i, device="cuda"))
+        q = api.quant_act(inputs.activations(N, K, seed=i + 99, device="cuda"))
+        assert torch.equal(api.linear(packed, alpha, *q), api.gemm(packed, alpha, *q)), (N, M, K)
+
+
+def test_linear_extreme_sums():
+    """The largest sums in magnitude: all weights +1 (or -1) against all codes
+    127 and -128 at the widest K, where the kernels' shifted sums just fit."""
+    K, M = 131072, 40
+    for c in (2, 0):                               # code + 1
+        word = sum(c << (2 * i) for i in range(16))
+        packed = torch.full((M, K // 16), word - (1 << 32 if word >> 31 else 0),
+                            dtype=torch.int32, device="cuda")
+        alpha = torch.ones(1, device="cuda")
+        for code in (127, -128):
+            for N in (1, 4, 20, 70, 140):
+                xq = torch.full((N, K), code, dtype=torch.int8, device="cuda")
+                amax = torch.full((N,), 127.0, device="cuda")
+                xsum = torch.full((N,), code * K, dtype=torch.int32, device="cuda")
+                y = api.linear(packed, alpha, xq, amax, xsum)
+                assert (y == float((c - 1) * code * K)).all(), (c, code, N)
+
+
+@pytest.mark.parametrize("N", [3, 40, 100, 300])
+def test_linear_wait_limit(N):
+    """A wait that runs out: the kernel returns, the error word says so, and the
+    same call with the default limit is right again.  80 row blocks of 1024
+    k-blocks, so that no cluster splits K: the accumulators take 100 us and more,
+    the limit is 2 us (a wait looks at the clock every eighth try)."""
+    M, K = 256 * 80, 131072
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    words = torch.from_numpy(np.random.RandomState(1).randint(0, 3, (64, 16)) @
+                             (4 ** np.arange(16, dtype=np.int64)))
+    words = torch.where(words >= 1 << 31, words - (1 << 32), words).to(torch.int32).cuda()
+    packed = words[torch.randint(0, 64, (M, K // 16), generator=g, device="cuda")]
+    alpha = torch.ones(1, device="cuda")
+    q = api.quant_act(inputs.activations(N, K, seed=4, device="cuda"))
+    want = api.gemm(packed, alpha, *q)
+    torch.cuda.synchronize()
+    assert _lib.bitlinear_device_error(clear=True) == _lib.OK
+    old = _lib.bitlinear_set_wait_limit(2000)
+    try:
+        api.linear(packed, alpha, *q)
+        torch.cuda.synchronize()
+    finally:
+        _lib.bitlinear_set_wait_limit(old)
+    assert _lib.bitlinear_device_error(clear=True) == _lib.ERR_DEVICE_TIMEOUT
+    assert torch.equal(api.linear(packed, alpha, *q), want)
+    assert _lib.bitlinear_device_error(clear=True) == _lib.OK
