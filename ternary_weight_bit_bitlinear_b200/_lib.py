@@ -177,6 +177,15 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def raw_stream(stream, device_index):
+    """The handle of `stream`, or of the device's current stream for None (as
+    an int; 2 us less per call than torch.cuda.current_stream())."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(device_index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
 # --------------------------------------------------------------- raw entry points
 # Each takes torch tensors (already allocated, on the current CUDA device) and
 # returns the C status code unchanged.

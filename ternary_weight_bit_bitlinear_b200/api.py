@@ -5,8 +5,6 @@ torch (device memory is torch's job here), and hands raw pointers to one C
 entry point of libbitlinear.so.  All arithmetic runs in the CUDA kernels;
 nothing here falls back to the CPU.
 """
-import contextlib
-
 import torch
 
 from . import _lib
@@ -354,6 +352,10 @@ def _activation(name):
                          % (sorted(k for k in ACTIVATIONS if k), name)) from None
 
 
+# The calls below run between the products of a decoded token, where the host's
+# time per call counts: each check first asks, in one expression, whether all is
+# well, and works out what is wrong only if it is not.
+
 def _need_rows(t, name, shape=None, dtype=None):
     """An activation matrix [N, K] of a known type whose rows are dense (the
     row stride is free).  Returns its row stride."""
@@ -364,51 +366,54 @@ def _need_rows(t, name, shape=None, dtype=None):
     if t.dtype not in ACT_DTYPES or (dtype is not None and t.dtype != dtype):
         raise TypeError("%s must be %s, got %s"
                         % (name, dtype or "float32, bfloat16 or float16", t.dtype))
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
         raise ValueError("%s must have shape %s, got %s"
                          % (name, shape or "[N, K]", tuple(t.shape)))
     N, K = t.shape
-    if K > 1 and t.stride(1) != 1:
+    ld, inner = t.stride()
+    if K > 1 and inner != 1:
         raise ValueError("%s must have dense rows (stride 1 along the last dimension)" % name)
-    ld = t.stride(0) if N > 1 else K
+    if N <= 1:
+        return K
     if ld < K:
         raise ValueError("%s: its rows overlap" % name)
     return ld
 
 
-def _need_vector(t, n, name, device):
-    """An optional fp32 vector of n entries on `device`."""
+def _vector_ptr(t, n, dtype, name, device):
+    """Pointer of a vector of n entries of `dtype` on `device`; None for None."""
     if t is None:
         return None
-    _need(t, torch.float32, name)
-    if t.numel() != n:
-        raise ValueError("%s must hold %d entries, got %d" % (name, n, t.numel()))
-    _on(device, **{name: t})
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.numel() == n
+            and t.device == device and t.is_cuda and t.is_contiguous()):
+        _need(t, dtype, name)
+        if t.numel() != n:
+            raise ValueError("%s must hold %d entries, got %d" % (name, n, t.numel()))
+        _on(device, **{name: t})
     return t.data_ptr()
 
 
-def _launch(dev, stream, call):
-    """call(raw stream) with `dev` current; raises on a status other than OK."""
+def _launch(fn, name, dev, stream, *args):
+    """fn(*args, raw stream) with `dev` current; raises on a status other than OK."""
     if torch.cuda.current_device() != dev.index:
         with torch.cuda.device(dev):
-            return call(_lib._stream(stream))
-    return call(_lib._stream(stream))
+            status = fn(*args, _lib.raw_stream(stream, dev.index))
+    else:
+        status = fn(*args, _lib.raw_stream(stream, dev.index))
+    if status != _lib.OK:
+        raise _lib.BitLinearError(status, name)
 
 
-def _out_stream(stream, dev):
-    """The context in which a call allocates what it returns: the stream that
-    writes it, so that the memory is not handed out again before that."""
+def _allocate(stream, dev, *shapes):
+    """Uninitialised tensors on `dev`, (shape, dtype) each, that belong to the
+    stream that will write them, so that their memory is not handed out again
+    before that."""
     if stream is None:
-        return contextlib.nullcontext()
+        return [torch.empty(s, dtype=d, device=dev) for s, d in shapes]
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=dev)
-    return torch.cuda.stream(stream)
-
-
-def _codes_out(N, K, dev):
-    return (torch.empty((N, K), dtype=torch.int8, device=dev),
-            torch.empty(N, dtype=torch.float32, device=dev),
-            torch.empty(N, dtype=torch.int32, device=dev))
+    with torch.cuda.stream(stream):
+        return [torch.empty(s, dtype=d, device=dev) for s, d in shapes]
 
 
 def norm_quant(x, weight=None, eps=1e-5, residual=None, normalize=True, h_out=None, stream=None):
@@ -424,34 +429,34 @@ def norm_quant(x, weight=None, eps=1e-5, residual=None, normalize=True, h_out=No
     gets amax NaN and codes 0.  Outputs belong to the stream that writes them.
     """
     ldx = _need_rows(x, "x")
-    N, K = x.shape
-    dev = x.device
+    shape, dtype, dev = x.shape, x.dtype, x.device
+    N, K = shape
     ldr = ldh = 0
+    rp = hp = None
     if residual is not None:
-        ldr = _need_rows(residual, "residual", (N, K), x.dtype)
-        _on(dev, residual=residual)
+        ldr = _need_rows(residual, "residual", shape, dtype)
+        rp = residual.data_ptr()
+        if residual.device != dev:
+            _on(dev, residual=residual)
         if h_out is not None:
-            _need_rows(h_out, "h_out", (N, K), x.dtype)
+            ldh = _need_rows(h_out, "h_out", shape, dtype)
             _on(dev, h_out=h_out)
     elif h_out is not None:
         raise ValueError("h_out without a residual: x itself is what the norm is taken of")
-    w = _need_vector(weight, K, "weight", dev)
-    if weight is not None and not normalize:
+    w = _vector_ptr(weight, K, torch.float32, "weight", dev)
+    if w is not None and not normalize:
         raise ValueError("weight belongs to the norm: pass None without it")
-    with _out_stream(stream, dev):
-        xq, amax, xsum = _codes_out(N, K, dev)
-        h = h_out
-        if residual is not None and h is None:
-            h = torch.empty((N, K), dtype=x.dtype, device=dev)
-    if h is not None:
-        ldh = h.stride(0) if N > 1 else K
-    a = _lib.Norm(x.data_ptr(), None if residual is None else residual.data_ptr(),
-                  None if h is None else h.data_ptr(), w, xq.data_ptr(), amax.data_ptr(),
-                  xsum.data_ptr(), N, K, ldx, ldr, ldh, eps, ACT_DTYPES[x.dtype],
-                  1 if normalize else 0)
-    _lib.check(_launch(dev, stream, lambda s: _lib.load().bitlinear_norm_quant(a, s)),
-               "bitlinear_norm_quant")
-    return (xq, amax, xsum) if residual is None else (h, xq, amax, xsum)
+    out = _allocate(stream, dev, (shape, torch.int8), (N, torch.float32), (N, torch.int32),
+                    *(((shape, dtype),) if rp is not None and h_out is None else ()))
+    xq, amax, xsum = out[:3]
+    if rp is not None:
+        if h_out is None:
+            h_out, ldh = out[3], K
+        hp = h_out.data_ptr()
+    a = _lib.Norm(x.data_ptr(), rp, hp, w, xq.data_ptr(), amax.data_ptr(), xsum.data_ptr(), N, K,
+                  ldx, ldr, ldh, eps, ACT_DTYPES[dtype], 1 if normalize else 0)
+    _launch(_lib.load().bitlinear_norm_quant, "bitlinear_norm_quant", dev, stream, a)
+    return (xq, amax, xsum) if residual is None else (h_out, xq, amax, xsum)
 
 
 def gated_norm_quant(gate, up, weight=None, eps=1e-5, activation="silu", normalize=True,
@@ -462,60 +467,75 @@ def gated_norm_quant(gate, up, weight=None, eps=1e-5, activation="silu", normali
     [N, 2K] buffer.  Returns (xq, amax, xsum), the input of the down
     projection."""
     ldg = _need_rows(gate, "gate")
-    N, K = gate.shape
-    dev = gate.device
-    ldu = _need_rows(up, "up", (N, K), gate.dtype)
-    _on(dev, up=up)
+    shape, dtype, dev = gate.shape, gate.dtype, gate.device
+    N, K = shape
+    ldu = _need_rows(up, "up", shape, dtype)
+    if up.device != dev:
+        _on(dev, up=up)
     act = _activation(activation)
-    w = _need_vector(weight, K, "weight", dev)
-    if weight is not None and not normalize:
+    w = _vector_ptr(weight, K, torch.float32, "weight", dev)
+    if w is not None and not normalize:
         raise ValueError("weight belongs to the norm: pass None without it")
-    with _out_stream(stream, dev):
-        xq, amax, xsum = _codes_out(N, K, dev)
+    xq, amax, xsum = _allocate(stream, dev, (shape, torch.int8), (N, torch.float32),
+                               (N, torch.int32))
     a = _lib.GatedNorm(gate.data_ptr(), up.data_ptr(), w, xq.data_ptr(), amax.data_ptr(),
-                       xsum.data_ptr(), N, K, ldg, ldu, eps, ACT_DTYPES[gate.dtype], act,
+                       xsum.data_ptr(), N, K, ldg, ldu, eps, ACT_DTYPES[dtype], act,
                        1 if normalize else 0)
-    _lib.check(_launch(dev, stream, lambda s: _lib.load().bitlinear_gated_norm_quant(a, s)),
-               "bitlinear_gated_norm_quant")
+    _launch(_lib.load().bitlinear_gated_norm_quant, "bitlinear_gated_norm_quant", dev, stream, a)
     return xq, amax, xsum
 
 
-def _linear_entry(packed, alpha, xq, amax, xsum, bias, activation, residual, out_dtype, out,
-                  stream):
-    """Checks one layer of a linear call; returns its entry and its output."""
-    _need(packed, torch.int32, "packed")
-    _need(alpha, torch.float32, "alpha")
-    _need(xq, torch.int8, "xq")
+def _codes_in(xq, amax, xsum, dev):
+    """Checks quantised activations; returns (N, K, their pointers)."""
+    if not (isinstance(xq, torch.Tensor) and xq.dtype is torch.int8 and xq.is_cuda
+            and xq.is_contiguous() and xq.device == dev):
+        _need(xq, torch.int8, "xq")
+        _on(dev, xq=xq)
     N, K = xq.shape
-    M = packed.shape[0]
-    _check_token_vector(amax, N, torch.float32, "amax")
-    _check_token_vector(xsum, N, torch.int32, "xsum")
-    if packed.shape[1] != packed_row_words(K):
+    _need_given(amax, "amax")
+    _need_given(xsum, "xsum")
+    return (N, K, xq.data_ptr(), _vector_ptr(amax, N, torch.float32, "amax", dev),
+            _vector_ptr(xsum, N, torch.int32, "xsum", dev))
+
+
+def _need_given(t, name):
+    if t is None:
+        raise TypeError("%s must be a torch.Tensor" % name)
+
+
+def _linear_entry(packed, alpha, dev, codes, bias, activation, residual, out_dtype, out, stream):
+    """Checks one layer of a linear call; returns its entry and its output."""
+    if not (isinstance(packed, torch.Tensor) and packed.dtype is torch.int32 and packed.is_cuda
+            and packed.is_contiguous() and packed.device == dev):
+        _need(packed, torch.int32, "packed")
+        _on(dev, packed=packed)
+    N, K, xq, amax, xsum = codes
+    M, words = packed.shape
+    if words != packed_row_words(K):
         raise ValueError("packed must be [M, packed_row_words(K)] = [%d, %d], got %s"
                          % (M, packed_row_words(K), tuple(packed.shape)))
-    dev = packed.device
-    _on(dev, alpha=alpha, xq=xq, amax=amax, xsum=xsum)
+    _need_given(alpha, "alpha")
     if out_dtype is None:
         out_dtype = (out.dtype if out is not None else
                      residual.dtype if residual is not None else torch.float32)
-    if out_dtype not in ACT_DTYPES:
+    code = ACT_DTYPES.get(out_dtype)
+    if code is None:
         raise TypeError("out_dtype must be float32, bfloat16 or float16, got %s" % out_dtype)
-    ldr = 0
+    ldr, rp = 0, None
     if residual is not None:
         ldr = _need_rows(residual, "residual", (N, M), out_dtype)
-        _on(dev, residual=residual)
+        rp = residual.data_ptr()
+        if residual.device != dev:
+            _on(dev, residual=residual)
     if out is None:
-        with _out_stream(stream, dev):
-            out = torch.empty((N, M), dtype=out_dtype, device=dev)
+        out, = _allocate(stream, dev, ((N, M), out_dtype))
         ldy = M
     else:
         ldy = _need_rows(out, "out", (N, M), out_dtype)
         _on(dev, out=out)
-    entry = (packed.data_ptr(), alpha.data_ptr(), M, K, xq.data_ptr(), amax.data_ptr(),
-             xsum.data_ptr(), _need_vector(bias, M, "bias", dev),
-             None if residual is None else residual.data_ptr(), out.data_ptr(), ldr, ldy,
-             ACT_DTYPES[out_dtype], _activation(activation))
-    return entry, out
+    return (packed.data_ptr(), _vector_ptr(alpha, 1, torch.float32, "alpha", dev), M, K, xq, amax,
+            xsum, _vector_ptr(bias, M, torch.float32, "bias", dev), rp, out.data_ptr(), ldr, ldy,
+            code, _activation(activation)), out
 
 
 def linear(packed, alpha, xq, amax, xsum, bias=None, activation=None, residual=None,
@@ -525,13 +545,13 @@ def linear(packed, alpha, xq, amax, xsum, bias=None, activation=None, residual=N
     (fp32, bf16 or fp16; by default the type of out, else of the residual,
     else fp32).  bias: fp32 [M]; residual and out: [N, M] of out_dtype with
     dense rows of any row stride; out may be the residual itself."""
-    entry, out = _linear_entry(packed, alpha, xq, amax, xsum, bias, activation, residual,
-                               out_dtype, out, stream)
-    arr = (_lib.LinearProblem * 1)(entry)
-    N = xq.shape[0]
-    _lib.check(_launch(packed.device, stream,
-                       lambda s: _lib.load().bitlinear_linear(arr, 1, N, s)),
-               "bitlinear_linear")
+    _need_given(packed, "packed")
+    dev = packed.device
+    codes = _codes_in(xq, amax, xsum, dev)
+    entry, out = _linear_entry(packed, alpha, dev, codes, bias, activation, residual, out_dtype,
+                               out, stream)
+    _launch(_lib.load().bitlinear_linear, "bitlinear_linear", dev, stream,
+            _lib.LinearProblem(*entry), 1, codes[0])
     return out
 
 
@@ -546,28 +566,32 @@ def linear_grouped(layers, xq, amax, xsum, bias=None, activation=None, residual=
         return []
 
     def each(v, name):
-        v = list(v) if isinstance(v, (list, tuple)) else [v] * n
+        if not isinstance(v, (list, tuple)):
+            return [v] * n
         if len(v) != n:
             raise ValueError("%s: one per layer, or one for all" % name)
         return v
 
     if outs is not None and not isinstance(outs, (list, tuple)):
         raise ValueError("outs: one per layer")
-    cols = [each(v, k) for v, k in ((xq, "xq"), (amax, "amax"), (xsum, "xsum"), (bias, "bias"),
-                                    (activation, "activation"), (residual, "residual"),
-                                    (out_dtype, "out_dtype"), (outs, "outs"))]
-    N, dev = cols[0][0].shape[0], layers[0][0].device
+    shared = not any(isinstance(v, (list, tuple)) for v in (xq, amax, xsum))
+    dev = layers[0][0].device
+    codes = _codes_in(xq, amax, xsum, dev) if shared else None
+    xqs, amaxs, xsums = each(xq, "xq"), each(amax, "amax"), each(xsum, "xsum")
+    biases, acts = each(bias, "bias"), each(activation, "activation")
+    residuals, dtypes = each(residual, "residual"), each(out_dtype, "out_dtype")
+    outs = each(outs, "outs")
     arr, ys = (_lib.LinearProblem * n)(), []
+    N = xqs[0].shape[0]
     for i, (packed, alpha) in enumerate(layers):
-        xqi, am, xs, b, act, res, dt, out = (c[i] for c in cols)
-        if xqi.shape[0] != N:
-            raise ValueError("layer %d: all layers share the token count" % i)
-        _on(dev, packed=packed)
-        entry, y = _linear_entry(packed, alpha, xqi, am, xs, b, act, res, dt, out, stream)
-        arr[i] = entry
+        if not shared:
+            codes = _codes_in(xqs[i], amaxs[i], xsums[i], dev)
+            if codes[0] != N:
+                raise ValueError("layer %d: all layers share the token count" % i)
+        arr[i], y = _linear_entry(packed, alpha, dev, codes, biases[i], acts[i], residuals[i],
+                                  dtypes[i], outs[i], stream)
         ys.append(y)
-    _lib.check(_launch(dev, stream, lambda s: _lib.load().bitlinear_linear(arr, n, N, s)),
-               "bitlinear_linear")
+    _launch(_lib.load().bitlinear_linear, "bitlinear_linear", dev, stream, arr, n, N)
     return ys
 
 

@@ -933,9 +933,12 @@ bitlinear_status bitlinear_norm_quant(const bitlinear_norm* a, bitlinear_stream_
   }
   const bl::NormParams p = {a->x,   a->residual, a->h,   a->weight, a->xq,
                             a->amax, a->xsum,    a->ldx, a->ldr,    a->ldh,
-                            a->eps, static_cast<int>(a->K), a->normalize ? 1 : 0,
-                            BITLINEAR_ACT_NONE};
-  return blh::launch_norm(false, static_cast<int>(a->N), a->dtype, p,
+                            a->eps, 1.0 / static_cast<double>(a->K), blh::wait_limit_ns(),
+                            static_cast<int>(a->K), 0,
+                            a->normalize ? 1 : 0, BITLINEAR_ACT_NONE};
+  DeviceInfo* dev = nullptr;
+  if ((st = device_info(&dev)) != BITLINEAR_OK) return st;
+  return blh::launch_norm(false, static_cast<int>(a->N), a->dtype, p, dev,
                           reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -950,9 +953,12 @@ bitlinear_status bitlinear_gated_norm_quant(const bitlinear_gated_norm* a,
   if ((st = check_rows(a->up, a->ldu, a->N, a->K, a->dtype)) != BITLINEAR_OK) return st;
   const bl::NormParams p = {a->gate, a->up,   nullptr, a->weight, a->xq,
                             a->amax, a->xsum, a->ldg,  a->ldu,    0,
-                            a->eps,  static_cast<int>(a->K), a->normalize ? 1 : 0,
-                            a->activation};
-  return blh::launch_norm(true, static_cast<int>(a->N), a->dtype, p,
+                            a->eps,  1.0 / static_cast<double>(a->K), blh::wait_limit_ns(),
+                            static_cast<int>(a->K), 0,
+                            a->normalize ? 1 : 0, a->activation};
+  DeviceInfo* dev = nullptr;
+  if ((st = device_info(&dev)) != BITLINEAR_OK) return st;
+  return blh::launch_norm(true, static_cast<int>(a->N), a->dtype, p, dev,
                           reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -1011,7 +1017,7 @@ bitlinear_status bitlinear_device_error(int* status_out, int clear) {
   v |= w;
   cudaError_t (*const readers[])(unsigned int*, bool) = {
       blh::device_error_gemv, blh::device_error_gemv_quant, blh::device_error_gemm,
-      blh::device_error_tl2};
+      blh::device_error_tl2,  blh::device_error_norm};
   for (auto rd : readers) {
     w = 0;
     if (rd(&w, clear != 0) != cudaSuccess) return BITLINEAR_ERR_CUDA;

@@ -64,6 +64,13 @@ __device__ __forceinline__ void store_vec(T* p, float (&f)[kVec<T>]) {
   *reinterpret_cast<uint4*>(p) = v.u;
 }
 
+// max(v, 0) that keeps a NaN.
+__device__ __forceinline__ float relu_nan(float v) {
+  float r;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(v));
+  return r;
+}
+
 // act(v), every operation a single fp32 rounding (no contraction):
 //   relu   max(v, 0)          relu2  max(v, 0)^2
 //   silu   v / (1 + e^-v)
@@ -72,9 +79,9 @@ __device__ __forceinline__ void store_vec(T* p, float (&f)[kVec<T>]) {
 // A NaN stays a NaN.
 __device__ __forceinline__ float activate(float v, int act) {
   switch (act) {
-    case BITLINEAR_ACT_RELU: return v < 0.0f ? 0.0f : v;
+    case BITLINEAR_ACT_RELU: return relu_nan(v);
     case BITLINEAR_ACT_RELU2: {
-      const float r = v < 0.0f ? 0.0f : v;
+      const float r = relu_nan(v);
       return __fmul_rn(r, r);
     }
     case BITLINEAR_ACT_SILU: return __fdiv_rn(v, __fadd_rn(1.0f, expf(-v)));
@@ -108,6 +115,25 @@ __device__ __forceinline__ float activate_product(float v, int act) {
     return __fdividef(v, __fadd_rn(1.0f, expf(-a)));
   }
   return activate(v, act);
+}
+
+// activate over n values, the choice made once.
+template <int n>
+__device__ __forceinline__ void activate_exact_all(float (&f)[n], int act) {
+  switch (act) {
+#define BL_ACT_ALL(a)                                                       \
+  case a: {                                                                 \
+    _Pragma("unroll") for (int i = 0; i < n; ++i) f[i] = activate(f[i], a); \
+    break;                                                                  \
+  }
+    BL_ACT_ALL(BITLINEAR_ACT_RELU)
+    BL_ACT_ALL(BITLINEAR_ACT_RELU2)
+    BL_ACT_ALL(BITLINEAR_ACT_SILU)
+    BL_ACT_ALL(BITLINEAR_ACT_GELU)
+    BL_ACT_ALL(BITLINEAR_ACT_GELU_TANH)
+#undef BL_ACT_ALL
+    default: break;
+  }
 }
 
 // activate_product over n values, the choice made once.

@@ -37,7 +37,7 @@ constexpr int kGemvWarps = 4;            // warps per CTA
 constexpr int kGemvThreads = kGemvWarps * 32;
 constexpr int kGemvMaxTokens = 16;
 constexpr int kGemvMaxProblems = 256;
-constexpr int kGemvEpMaxProblems = 64;
+constexpr int kGemvEpMaxProblems = 16;
 constexpr int kGemvEpMaxTokens = 8;
 
 template <int NT>

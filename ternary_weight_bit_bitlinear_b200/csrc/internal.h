@@ -26,6 +26,13 @@ namespace blh {
 
 constexpr int kMaxDevices = 64;
 
+// A row kernel of norm.cuh: set up, and its CTAs per SM at the last
+// shared-memory size asked about.
+struct NormKernelInfo {
+  bool set = false;
+  int smem = 0, per_sm = 0;
+};
+
 // Per-device facts and one-time set-up flags, looked up once per device.
 struct DeviceInfo {
   int sms = 0;
@@ -39,6 +46,7 @@ struct DeviceInfo {
   bool gemv_split_attr_set[bl::kGemvMaxTokens + 1] = {};
   int gemv_ep_blocks_per_sm[bl::kGemvEpMaxTokens + 1] = {};     // 0: not set up yet
   bool gemv_ep_split_attr_set[bl::kGemvEpMaxTokens + 1] = {};
+  NormKernelInfo norm[3][2][3];       // type, gated, threads (128, 256, 512)
   bool split_attr_set[3] = {};        // gemm_split_kernel: 32, 64, 128 tokens
   int split_clusters[3][3] = {};      // resident clusters of 1, 2, 4 pairs; 0: not asked yet
 };
@@ -80,9 +88,9 @@ bitlinear_status launch_gemv(int N, const bl::GemvParams& p, DeviceInfo* dev, cu
 bitlinear_status launch_gemv_ep(int N, const bl::GemvEpParams& p, DeviceInfo* dev,
                                 cudaStream_t s);
 
-// launch_norm.cu: row operators between two products, one CTA per row.
+// launch_norm.cu: row operators between two products.
 bitlinear_status launch_norm(bool gated, int rows, int dtype, const bl::NormParams& p,
-                             cudaStream_t s);
+                             DeviceInfo* dev, cudaStream_t s);
 
 // launch_gemv_quant.cu: the fused quantise + GEMV decode kernel.  CTAs of
 // `warps` warps with `area` bytes of dynamic shared memory each.
@@ -116,6 +124,7 @@ cudaError_t device_error_gemv(unsigned int* v, bool clear);
 cudaError_t device_error_gemv_quant(unsigned int* v, bool clear);
 cudaError_t device_error_gemm(unsigned int* v, bool clear);
 cudaError_t device_error_tl2(unsigned int* v, bool clear);
+cudaError_t device_error_norm(unsigned int* v, bool clear);
 
 // Shared body of the device_error_* readers (each unit passes its own symbol).
 template <typename Sym>

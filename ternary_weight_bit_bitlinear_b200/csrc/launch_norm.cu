@@ -6,36 +6,112 @@
 namespace blh {
 namespace {
 
+// Rows up to 32 * kThreads wide: one CTA per row at a time, as many CTAs as
+// are resident.
+template <typename T, int kThreads, bool kGated>
+bitlinear_status launch_stream(int rows, const bl::NormParams& p, NormKernelInfo& known, int sms,
+                               cudaStream_t s) {
+  auto kernel = bl::norm_stream_kernel<T, kThreads, kGated>;
+  constexpr int most = 2 * kThreads * bl::kNormRegElems * static_cast<int>(sizeof(T));
+  const int smem = p.K * static_cast<int>(sizeof(T)) * (kGated || p.b ? 2 : 1);
+  if (!known.set) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) !=
+        cudaSuccess)
+      return BITLINEAR_ERR_CUDA;
+    known.set = true;
+  }
+  int grid = rows;
+  if (rows > sms) {
+    int per_sm = known.per_sm;
+    if (per_sm == 0 || known.smem != smem) {
+      if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, smem) !=
+              cudaSuccess ||
+          per_sm < 1)
+        return BITLINEAR_ERR_CUDA;
+      known.smem = smem;
+      known.per_sm = per_sm;
+    }
+    if (grid > sms * per_sm) grid = sms * per_sm;
+  }
+  if (launch_pdl(kernel, grid, kThreads, smem, s, p, rows) != cudaSuccess)
+    return BITLINEAR_ERR_CUDA;
+  return launch_status();
+}
+
+// Wider rows: a cluster of C CTAs per row, at most 2^31 - 1 CTAs per launch.
+template <typename T, int kThreads, bool kGated>
+bitlinear_status launch_cluster(int64_t rows, int C, bl::NormParams p, cudaStream_t s) {
+  p.slice = (p.K / bl::kVec<T> + C - 1) / C;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(C);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  constexpr int64_t most = int64_t(1) << 27;
+  for (int64_t done = 0; done < rows; done += most) {
+    const int64_t n = rows - done < most ? rows - done : most;
+    bl::NormParams q = p;
+    q.a = static_cast<const T*>(p.a) + done * p.lda;
+    if (p.b) q.b = static_cast<const T*>(p.b) + done * p.ldb;
+    if (p.h) q.h = static_cast<T*>(p.h) + done * p.ldh;
+    q.xq = p.xq + done * p.K;
+    q.amax = p.amax + done;
+    if (p.xsum) q.xsum = p.xsum + done;
+    cfg.gridDim = dim3(static_cast<unsigned>(n * C));
+    if (cudaLaunchKernelEx(&cfg, bl::norm_quant_kernel<T, kThreads, kGated>, q) != cudaSuccess)
+      return BITLINEAR_ERR_CUDA;
+  }
+  return launch_status();
+}
+
+// The narrowest CTA that holds a row in registers (one warp more costs every
+// row its share of the reductions: 2048 x 4096 bf16 with 128 / 256 / 512
+// threads 14.6 / 17.7 / 29.7 us).  From 16384 elements on that would be 1024
+// threads of 64 registers, which spill: clusters there, of 8 CTAs while the
+// rows leave SMs idle (one row of 28672: 4.6 us; 256 rows: 31.8 with 4 x 256
+// threads, 49.2 with 8 x 512), and where 4 x 256 threads do not hold the row.
 template <typename T, bool kGated>
-bitlinear_status launch_norm_type(int rows, const bl::NormParams& p, cudaStream_t s) {
-  // The fewest threads that hold the row in registers.
-  cudaError_t e;
+bitlinear_status launch_norm_type(int rows, const bl::NormParams& p, DeviceInfo* dev, int type,
+                                  cudaStream_t s) {
+  NormKernelInfo* known = dev->norm[type][kGated ? 1 : 0];
   if (p.K <= 128 * bl::kNormRegElems)
-    e = launch_pdl(bl::norm_quant_kernel<T, 128, kGated>, rows, 128, 0, s, p);
-  else if (p.K <= 256 * bl::kNormRegElems)
-    e = launch_pdl(bl::norm_quant_kernel<T, 256, kGated>, rows, 256, 0, s, p);
-  else if (p.K <= 512 * bl::kNormRegElems)
-    e = launch_pdl(bl::norm_quant_kernel<T, 512, kGated>, rows, 512, 0, s, p);
-  else
-    e = launch_pdl(bl::norm_quant_kernel<T, 1024, kGated>, rows, 1024, 0, s, p);
-  return e == cudaSuccess ? launch_status() : BITLINEAR_ERR_CUDA;
+    return launch_stream<T, 128, kGated>(rows, p, known[0], dev->sms, s);
+  if (p.K <= 256 * bl::kNormRegElems)
+    return launch_stream<T, 256, kGated>(rows, p, known[1], dev->sms, s);
+  if (p.K <= 512 * bl::kNormRegElems)
+    return launch_stream<T, 512, kGated>(rows, p, known[2], dev->sms, s);
+  if (p.K > 4 * 256 * bl::kNormRegElems || rows * int64_t(8) <= dev->sms)
+    return launch_cluster<T, 512, kGated>(rows, 8, p, s);
+  return launch_cluster<T, 256, kGated>(rows, 4, p, s);
 }
 
 template <bool kGated>
-bitlinear_status launch_norm_any(int rows, int dtype, const bl::NormParams& p, cudaStream_t s) {
+bitlinear_status launch_norm_any(int rows, int dtype, const bl::NormParams& p, DeviceInfo* dev,
+                                 cudaStream_t s) {
   switch (dtype) {
-    case BITLINEAR_F32: return launch_norm_type<float, kGated>(rows, p, s);
-    case BITLINEAR_BF16: return launch_norm_type<__nv_bfloat16, kGated>(rows, p, s);
-    default: return launch_norm_type<__half, kGated>(rows, p, s);
+    case BITLINEAR_F32: return launch_norm_type<float, kGated>(rows, p, dev, 0, s);
+    case BITLINEAR_BF16: return launch_norm_type<__nv_bfloat16, kGated>(rows, p, dev, 1, s);
+    default: return launch_norm_type<__half, kGated>(rows, p, dev, 2, s);
   }
 }
 
 }  // namespace
 
 bitlinear_status launch_norm(bool gated, int rows, int dtype, const bl::NormParams& p,
-                             cudaStream_t s) {
-  return gated ? launch_norm_any<true>(rows, dtype, p, s)
-               : launch_norm_any<false>(rows, dtype, p, s);
+                             DeviceInfo* dev, cudaStream_t s) {
+  return gated ? launch_norm_any<true>(rows, dtype, p, dev, s)
+               : launch_norm_any<false>(rows, dtype, p, dev, s);
+}
+
+cudaError_t device_error_norm(unsigned int* v, bool clear) {
+  return read_error_word(bl::g_device_error, v, clear);
 }
 
 }  // namespace blh

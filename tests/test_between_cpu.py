@@ -170,7 +170,8 @@ def test_python_refusals_on_device():
     with pytest.raises(ValueError, match="64"):
         api.norm_quant(x, torch.ones(65, device="cuda"))
     with pytest.raises(ValueError, match="device"):
-        api._need_vector(torch.ones(64, device="cuda"), 64, "weight", torch.device("cuda", 1))
+        api._vector_ptr(torch.ones(64, device="cuda"), 64, torch.float32, "weight",
+                        torch.device("cuda", 1))
     with pytest.raises(_lib.BitLinearError):
         api.norm_quant(x[:, 1:49])                    # rows not on 16 bytes
     with pytest.raises(_lib.BitLinearError):

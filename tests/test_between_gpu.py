@@ -502,3 +502,63 @@ def test_linear_wait_limit(N):
     assert _lib.bitlinear_device_error(clear=True) == _lib.ERR_DEVICE_TIMEOUT
     assert torch.equal(api.linear(packed, alpha, *q), want)
     assert _lib.bitlinear_device_error(clear=True) == _lib.OK
+
+
+@pytest.mark.parametrize("N,K", [(400, 2048), (3, 28672), (40, 28672), (2, 65536)])
+def test_norm_wait_limit(N, K):
+    """With a limit of a nanosecond the row kernels' waits may run out or not;
+    they return either way, and the default limit is right again."""
+    x = rows(N, K, 9, torch.bfloat16).contiguous()
+    want = ref.norm_rows(f32(x), None, EPS)
+    old = _lib.bitlinear_set_wait_limit(1)
+    try:
+        api.norm_quant(x, eps=EPS)
+        api.gated_norm_quant(x, x, eps=EPS)
+        torch.cuda.synchronize()
+    finally:
+        _lib.bitlinear_set_wait_limit(old)
+    assert _lib.bitlinear_device_error(clear=True) in (_lib.OK, _lib.ERR_DEVICE_TIMEOUT)
+    check_codes(api.norm_quant(x, eps=EPS), want)
+    assert _lib.bitlinear_device_error(clear=True) == _lib.OK
+
+
+def test_norm_rows_beyond_32_bit_offsets():
+    """Row offsets past 2^31 elements: views with a large row stride."""
+    K, N, ld = 1024, 3, (1 << 30) + 64                # 2 * ld elements from first to last row
+    if torch.cuda.mem_get_info()[0] < 12 << 30:
+        pytest.skip("needs 12 GB")
+    buf = torch.empty(2 * ld + K, dtype=torch.bfloat16, device="cuda")
+    x = buf.as_strided((N, K), (ld, 1))
+    x.copy_(rows(N, K, 5, torch.bfloat16))
+    w = weight(K, 6)
+    check_codes(api.norm_quant(x, w, eps=EPS), ref.norm_rows(f32(x), w.cpu().numpy(), EPS))
+    h, *got = api.norm_quant(x.contiguous(), w, eps=EPS, residual=x.contiguous(), h_out=x)
+    check_codes(got, ref.norm_rows(f32(h), w.cpu().numpy(), EPS))
+    assert h.data_ptr() == buf.data_ptr()
+    packed, alpha, xq, amax, xsum, acc = product(40, 272, N, 8)
+    for n in (1, 3):
+        y = api.linear(packed, alpha, xq[:n], amax[:n], xsum[:n], out=x[:n, :40],
+                       residual=x[:n, 40:80])
+        check_linear(y, acc[:n], alpha, amax[:n], None, None, x[:n, 40:80], torch.bfloat16)
+
+
+def test_norm_many_rows():
+    """More rows than resident CTAs, several of each CTA's, all types."""
+    for dtype in DTYPES:
+        x, res, w = rows(5000, 272, 3, dtype), rows(5000, 272, 4, dtype), weight(272, 5)
+        h, *got = api.norm_quant(x, w, eps=EPS, residual=res)
+        check_codes(got, ref.norm_rows(f32(h), w.cpu().numpy(), EPS))
+
+
+def test_two_streams_at_once():
+    """Calls on two streams share no workspace: each gives what it gives alone."""
+    mlps = [Mlp(512, 1408, 60), Mlp(512, 1408, 70)]
+    ins = [(rows(64, 512, i, torch.bfloat16), rows(64, 512, i + 1, torch.bfloat16))
+           for i in (1, 3)]
+    want = [m(*i) for m, i in zip(mlps, ins)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in mlps]
+    for _ in range(10):
+        got = [m(*i, stream=s) for m, i, s in zip(mlps, ins, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, w) for g, w in zip(got, want))
