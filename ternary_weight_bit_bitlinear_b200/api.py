@@ -404,16 +404,16 @@ def _launch(fn, name, dev, stream, *args):
         raise _lib.BitLinearError(status, name)
 
 
-def _allocate(stream, dev, *shapes):
-    """Uninitialised tensors on `dev`, (shape, dtype) each, that belong to the
-    stream that will write them, so that their memory is not handed out again
-    before that."""
+def _allocate(stream, like, *shapes):
+    """Uninitialised tensors beside `like`, (shape, dtype) each, that belong to
+    the stream that will write them, so that their memory is not handed out
+    again before that."""
     if stream is None:
-        return [torch.empty(s, dtype=d, device=dev) for s, d in shapes]
+        return [like.new_empty(s, dtype=d) for s, d in shapes]
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
     with torch.cuda.stream(stream):
-        return [torch.empty(s, dtype=d, device=dev) for s, d in shapes]
+        return [like.new_empty(s, dtype=d) for s, d in shapes]
 
 
 def norm_quant(x, weight=None, eps=1e-5, residual=None, normalize=True, h_out=None, stream=None):
@@ -446,7 +446,7 @@ def norm_quant(x, weight=None, eps=1e-5, residual=None, normalize=True, h_out=No
     w = _vector_ptr(weight, K, torch.float32, "weight", dev)
     if w is not None and not normalize:
         raise ValueError("weight belongs to the norm: pass None without it")
-    out = _allocate(stream, dev, (shape, torch.int8), (N, torch.float32), (N, torch.int32),
+    out = _allocate(stream, x, (shape, torch.int8), (N, torch.float32), (N, torch.int32),
                     *(((shape, dtype),) if rp is not None and h_out is None else ()))
     xq, amax, xsum = out[:3]
     if rp is not None:
@@ -476,7 +476,7 @@ def gated_norm_quant(gate, up, weight=None, eps=1e-5, activation="silu", normali
     w = _vector_ptr(weight, K, torch.float32, "weight", dev)
     if w is not None and not normalize:
         raise ValueError("weight belongs to the norm: pass None without it")
-    xq, amax, xsum = _allocate(stream, dev, (shape, torch.int8), (N, torch.float32),
+    xq, amax, xsum = _allocate(stream, gate, (shape, torch.int8), (N, torch.float32),
                                (N, torch.int32))
     a = _lib.GatedNorm(gate.data_ptr(), up.data_ptr(), w, xq.data_ptr(), amax.data_ptr(),
                        xsum.data_ptr(), N, K, ldg, ldu, eps, ACT_DTYPES[dtype], act,
@@ -528,7 +528,7 @@ def _linear_entry(packed, alpha, dev, codes, bias, activation, residual, out_dty
         if residual.device != dev:
             _on(dev, residual=residual)
     if out is None:
-        out, = _allocate(stream, dev, ((N, M), out_dtype))
+        out, = _allocate(stream, packed, ((N, M), out_dtype))
         ldy = M
     else:
         ldy = _need_rows(out, "out", (N, M), out_dtype)

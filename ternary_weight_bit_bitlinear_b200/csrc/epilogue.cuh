@@ -136,8 +136,8 @@ struct EpRows {
       return;
     }
     if (m >= M) return;
-    const T* r = static_cast<const T*>(e.residual) + m;
-    T* y = static_cast<T*>(e.y) + m;
+    const T* r = static_cast<const T*>(e.residual) + static_cast<int64_t>(n0) * e.ldr + m;
+    T* y = static_cast<T*>(e.y) + static_cast<int64_t>(n0) * e.ldy + m;
     const int nt = min(kTokens, N - n0);
 #pragma unroll 1
     for (int j0 = 0; j0 < nt; j0 += 8) {
@@ -145,16 +145,18 @@ struct EpRows {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         f[j] = j0 + j < kTokens ? blk[(j0 + j) * 32 + lane] : 0.0f;
-        g[j] = e.residual && j0 + j < nt
-                   ? Elem<T>::to_float(r[static_cast<int64_t>(n0 + j0 + j) * e.ldr]) : 0.0f;
+        g[j] = 0.0f;
+        if (e.residual) {
+          if (j0 + j < nt) g[j] = Elem<T>::to_float(*r);
+          r += e.ldr;
+        }
         if (e.bias) f[j] = __fadd_rn(f[j], bias[0]);
       }
       activate_all(f, e.act);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        if (j0 + j < nt)
-          y[static_cast<int64_t>(n0 + j0 + j) * e.ldy] =
-              Elem<T>::from_float(e.residual ? __fadd_rn(f[j], g[j]) : f[j]);
+        if (j0 + j < nt) *y = Elem<T>::from_float(e.residual ? __fadd_rn(f[j], g[j]) : f[j]);
+        y += e.ldy;
       }
     }
   }
