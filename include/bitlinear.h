@@ -396,7 +396,8 @@ typedef struct {
  * Root-mean-square norm with the residual's addition, and int8 output with one
  * scale per token (the quantiser of bitlinear_quant_act behind it):
  *   h    = x, or with a residual x + residual rounded to dtype (written out)
- *   r    = 1 / sqrt(sum_k h^2 / K + eps)     in 64 bits, rounded once to fp32
+ *   r    = 1 / sqrt(sum_k h^2 / K + eps)     in 64 bits, rounded once to fp32:
+ *          it does not depend on the order of the sum, nor do the codes
  *   v    = (h * r) * weight                   (v = h when normalize is 0)
  *   amax = max_k |v|;  xq, xsum as in bitlinear_quant_act
  * eps must be positive and finite, and weight NULL without the norm.  A row
@@ -456,9 +457,11 @@ typedef struct {
  * The ternary product with its epilogue, over a list of layers that share the
  * token count (as bitlinear_gemm_grouped does):
  *   y[n,m] = act(acc[n,m] * (alpha * (amax[n]/127)) + bias[m]) + residual[n,m]
- * in fp32, rounded once to dtype.  Any N: one token runs on the CUDA cores,
- * more on the tensor cores.  y may be the residual itself (same pointer and
- * stride); any other overlap is an error of the caller.
+ * in fp32, rounded once to dtype; the divisions of silu and gelu_tanh are
+ * within 2 units in the last place.  Any N: a few tokens run on the CUDA cores,
+ * more on the tensor cores.  The layers of a call do not wait for one another.
+ * y may be the residual itself (same pointer and stride); any other overlap is
+ * an error of the caller.
  * bias 4-byte aligned; residual and y aligned to an element, row strides (when
  * N > 1) at least M; the other pointers as in bitlinear_gemm.  `problems` is a
  * HOST array read during the call only; all layers are checked before

@@ -391,9 +391,11 @@ def test_mlp_block(N):
     assert np.array_equal(y.cpu().numpy(), mlp.plain(f32(x), f32(res)))
 
 
-def test_mlp_block_on_another_stream_and_in_a_graph():
+# one token and five: CUDA cores; 40 and 150: tensor cores
+@pytest.mark.parametrize("N", [1, 5, 40, 150])
+def test_mlp_block_on_another_stream_and_in_a_graph(N):
     mlp = Mlp(256, 704, 50)
-    x, res = rows(5, 256, 1, torch.bfloat16), rows(5, 256, 2, torch.bfloat16)
+    x, res = rows(N, 256, 1, torch.bfloat16), rows(N, 256, 2, torch.bfloat16)
     want = mlp(x, res)
     torch.cuda.synchronize()
     s = torch.cuda.Stream()
@@ -404,10 +406,11 @@ def test_mlp_block_on_another_stream_and_in_a_graph():
             again = mlp(x, res)                    # and by context
         s.synchronize()
         assert torch.equal(got, want) and torch.equal(again, want)
+    assert torch.equal(mlp(x, res, stream=s.cuda_stream), want)    # a raw handle
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         y = mlp(x, res)
-    x2, res2 = rows(5, 256, 3, torch.bfloat16), rows(5, 256, 4, torch.bfloat16)
+    x2, res2 = rows(N, 256, 3, torch.bfloat16), rows(N, 256, 4, torch.bfloat16)
     want2 = mlp(x2, res2)
     x.copy_(x2)
     res.copy_(res2)
@@ -562,3 +565,68 @@ def test_two_streams_at_once():
         got = [m(*i, stream=s) for m, i, s in zip(mlps, ins, streams)]
         torch.cuda.synchronize()
         assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
+FIRST_CALL = """
+import torch
+from ternary_weight_bit_bitlinear_b200 import api, inputs
+packed, alpha = api.pack_weights(inputs.latent_weights(512, 1024, seed=1, device="cuda"))
+x = inputs.activations(40, 1024, seed=2, device="cuda")
+wide = inputs.activations(40, 20480, seed=3, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    q = api.norm_quant(x)
+    ys = [api.linear(packed, alpha, *(t[:n] for t in q)) for n in (1, 3, 40)]
+    z = api.gated_norm_quant(wide, wide)
+g.replay()
+torch.cuda.synchronize()
+for got, want in zip(q, api.norm_quant(x)):
+    assert torch.equal(got, want)
+for n, y in zip((1, 3, 40), ys):
+    assert torch.equal(y, api.matmul(packed, alpha, *(t[:n] for t in q)))
+for got, want in zip(z, api.gated_norm_quant(wide, wide)):
+    assert torch.equal(got, want)
+print("captured")
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    """What a call looks up once per device (attributes, occupancy) can be
+    looked up while a graph is being captured."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True,
+                         text=True, timeout=300)
+    assert out.returncode == 0 and "captured" in out.stdout, out.stderr[-2000:]
+
+
+def test_host_threads_at_once():
+    """Two host threads, each on its own stream, of sizes that make the
+    once-per-device caches change hands."""
+    import threading
+    packed, alpha = api.pack_weights(inputs.latent_weights(640, 1024, seed=1, device="cuda"))
+    xs = [rows(400, 1024, i, torch.bfloat16).contiguous() for i in (1, 2)]
+    want = [api.linear(packed, alpha, *api.norm_quant(x), out_dtype=torch.bfloat16) for x in xs]
+    other = [api.norm_quant(x[:, :512 * (i + 1)].contiguous()) for i, x in enumerate(xs)]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(50):
+                y = api.linear(packed, alpha, *api.norm_quant(xs[i]), out_dtype=torch.bfloat16)
+                o = api.norm_quant(xs[i][:, :512 * (i + 1)].contiguous())
+                s.synchronize()
+                if not torch.equal(y, want[i]) or not all(map(torch.equal, o, other[i])):
+                    bad.append(i)
+
+    ts = [threading.Thread(target=work, args=(i,)) for i in (0, 1)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    assert not bad
