@@ -6,13 +6,13 @@
 namespace blh {
 namespace {
 
-// Rows up to 32 * kThreads wide: one CTA per row at a time, as many CTAs as
+// Rows up to kElems * kThreads wide: one CTA per row at a time, as many CTAs as
 // are resident.
-template <typename T, int kThreads, bool kGated>
+template <typename T, int kThreads, int kElems, bool kGated>
 bitlinear_status launch_stream(int rows, const bl::NormParams& p, NormKernelInfo& known, int sms,
                                cudaStream_t s) {
-  auto kernel = bl::norm_stream_kernel<T, kThreads, kGated>;
-  constexpr int most = 2 * kThreads * bl::kNormRegElems * static_cast<int>(sizeof(T));
+  auto kernel = bl::norm_stream_kernel<T, kThreads, kElems, kGated>;
+  constexpr int most = 2 * kThreads * kElems * static_cast<int>(sizeof(T));
   const int smem = p.K * static_cast<int>(sizeof(T)) * (kGated || p.b ? 2 : 1);
   if (!known.set) {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) !=
@@ -39,7 +39,7 @@ bitlinear_status launch_stream(int rows, const bl::NormParams& p, NormKernelInfo
 }
 
 // Wider rows: a cluster of C CTAs per row, at most 2^31 - 1 CTAs per launch.
-template <typename T, int kThreads, bool kGated>
+template <typename T, int kThreads, int kElems, bool kGated>
 bitlinear_status launch_cluster(int64_t rows, int C, bl::NormParams p, cudaStream_t s) {
   p.slice = (p.K / bl::kVec<T> + C - 1) / C;
   cudaLaunchConfig_t cfg = {};
@@ -65,7 +65,7 @@ bitlinear_status launch_cluster(int64_t rows, int C, bl::NormParams p, cudaStrea
     q.amax = p.amax + done;
     if (p.xsum) q.xsum = p.xsum + done;
     cfg.gridDim = dim3(static_cast<unsigned>(n * C));
-    if (cudaLaunchKernelEx(&cfg, bl::norm_quant_kernel<T, kThreads, kGated>, q) != cudaSuccess)
+    if (cudaLaunchKernelEx(&cfg, bl::norm_quant_kernel<T, kThreads, kElems, kGated>, q) != cudaSuccess)
       return BITLINEAR_ERR_CUDA;
   }
   return launch_status();
@@ -73,23 +73,31 @@ bitlinear_status launch_cluster(int64_t rows, int C, bl::NormParams p, cudaStrea
 
 // The narrowest CTA that holds a row in registers (one warp more costs every
 // row its share of the reductions: 2048 x 4096 bf16 with 128 / 256 / 512
-// threads 14.6 / 17.7 / 29.7 us).  From 16384 elements on that would be 1024
-// threads of 64 registers, which spill: clusters there, of 8 CTAs while the
-// rows leave SMs idle (one row of 28672: 4.6 us; 256 rows: 31.8 with 4 x 256
-// threads, 49.2 with 8 x 512), and where 4 x 256 threads do not hold the row.
+// threads 14.6 / 17.7 / 29.7 us), with few registers a thread past the row's
+// end (their zeros run through all of the arithmetic: 2048 x 2560 bf16 in
+// 160 threads of 16 values 10.2 us, in 128 of 32 12.2; 512 rows 4.7 and 5.6).
+// From 16384 elements on that would be 1024 threads of 64 registers, which
+// spill: clusters there, of 8 CTAs while the rows leave SMs idle (one row of
+// 28672: 4.0 us; 256 rows: 31 with 4 x 256 threads, 49 with 8 x 512), and
+// where 4 x 256 threads do not hold the row.
 template <typename T, bool kGated>
 bitlinear_status launch_norm_type(int rows, const bl::NormParams& p, DeviceInfo* dev, int type,
                                   cudaStream_t s) {
   NormKernelInfo* known = dev->norm[type][kGated ? 1 : 0];
-  if (p.K <= 128 * bl::kNormRegElems)
-    return launch_stream<T, 128, kGated>(rows, p, known[0], dev->sms, s);
-  if (p.K <= 256 * bl::kNormRegElems)
-    return launch_stream<T, 256, kGated>(rows, p, known[1], dev->sms, s);
-  if (p.K <= 512 * bl::kNormRegElems)
-    return launch_stream<T, 512, kGated>(rows, p, known[2], dev->sms, s);
-  if (p.K > 4 * 256 * bl::kNormRegElems || rows * int64_t(8) <= dev->sms)
-    return launch_cluster<T, 512, kGated>(rows, 8, p, s);
-  return launch_cluster<T, 256, kGated>(rows, 4, p, s);
+  const int K = p.K, sms = dev->sms;
+  if (K <= 1024) return launch_stream<T, 128, 8, kGated>(rows, p, known[0], sms, s);
+  if (K <= 2048) return launch_stream<T, 128, 16, kGated>(rows, p, known[1], sms, s);
+  if (K <= 2560) return launch_stream<T, 160, 16, kGated>(rows, p, known[2], sms, s);
+  if (K <= 4096) return launch_stream<T, 128, 32, kGated>(rows, p, known[3], sms, s);
+  if (K <= 6144) return launch_stream<T, 256, 24, kGated>(rows, p, known[4], sms, s);
+  if (K <= 8192) return launch_stream<T, 256, 32, kGated>(rows, p, known[5], sms, s);
+  if (K <= 12288) return launch_stream<T, 512, 24, kGated>(rows, p, known[6], sms, s);
+  if (K <= 16384) return launch_stream<T, 512, 32, kGated>(rows, p, known[7], sms, s);
+  if (K <= 32768 && rows * int64_t(8) > sms)
+    return launch_cluster<T, 256, 32, kGated>(rows, 4, p, s);
+  if (K <= 32768) return launch_cluster<T, 512, 8, kGated>(rows, 8, p, s);
+  if (K <= 65536) return launch_cluster<T, 512, 16, kGated>(rows, 8, p, s);
+  return launch_cluster<T, 512, 32, kGated>(rows, 8, p, s);
 }
 
 template <bool kGated>

@@ -11,11 +11,11 @@
 // The sum of squares and r are held in 64 bits and r is rounded once (squares
 // of fp32 values are exact there), so r, and with it every code, does not
 // depend on how the row is cut into threads: the result is the definition's,
-// as it is for the library's other integer results.  The maximum
-// keeps inf and NaN: a row that holds either gets amax = NaN and q = 0.
+// as it is for the library's other integer results.  The maximum keeps inf and
+// NaN: a row that holds either gets amax = NaN and q = 0.
 //
 // Two kernels, both reading each element once and holding it in registers from
-// the load to the codes (kNormRegElems per thread):
+// the load to the codes (kElems per thread, 8 to 32):
 //   norm_stream_kernel  rows up to 16384 wide, one CTA per row: persistent CTAs
 //                       whose next row is on its way into shared memory while
 //                       the present one goes through its sum and its maximum;
@@ -26,12 +26,12 @@
 //                       receiver counts.
 // The waits are bounded, as everywhere.
 //
-// Bound by memory in fp32 with a residual (2048 x 8192: 38.4 us, 5.7 TB/s of
+// Bound by memory in fp32 with a residual (2048 x 8192: 37.6 us, 5.8 TB/s of
 // the 13 bytes an element), by instructions where the elements are 16 bits
-// wide (2048 x 4096 bf16 with a residual: 14.6 us, 4.0 TB/s; gate and up
-// 2048 x 6912: 22.6 us, 3.1 TB/s): some 20 per element, the conversion to 64
-// bits among them (16 a cycle and SM).  One token: 2.6 us at 2560, 3.4 at
-// 8192 (launch to launch), 4.6 at 28672, where one CTA would take 14.6.
+// wide (2048 x 4096 bf16 with a residual: 13.2 us, 4.4 TB/s; gate and up
+// 2048 x 6912: 22.9 us, 3.1 TB/s): some 20 per element, the conversion to 64
+// bits among them (16 a cycle and SM).  One token: 2.5 us at 2560, 3.2 at
+// 8192 (launch to launch), 4.0 at 28672, where one CTA would take 14.6.
 #pragma once
 
 #include "element.cuh"
@@ -40,7 +40,7 @@
 
 namespace bl {
 
-constexpr int kNormRegElems = 32;   // values of the row each thread keeps
+constexpr int kNormRegElems = 32;   // the most values of a row that a thread keeps
 
 struct NormParams {
   const void* a;          // x, or gate
@@ -74,23 +74,29 @@ __device__ __forceinline__ float norm_rsqrt(double t) {
   return static_cast<float>(1.0 / sqrt(t));
 }
 
-// The 16 bytes of x or gate, and of residual or up, that make chunk c of a row.
+// A thread's chunks past the end of its row hold zeros, which change no sum and
+// no maximum: everything but loads and stores runs without a condition, so the
+// instructions of different chunks interleave.
+
+// The 16 bytes of x or gate, and of residual or up, that make chunk c of a row;
+// zeros unless `in`.
 struct NormRaw {
   uint4 a, b;
 };
 
-template <typename T, bool kGated>
-__device__ __forceinline__ NormRaw norm_fetch(const T* a, const T* b, int c) {
+template <typename T>
+__device__ __forceinline__ NormRaw norm_fetch(const T* a, const T* b, int c, bool in, bool two) {
   NormRaw v;
-  v.a = *(reinterpret_cast<const uint4*>(a) + c);
-  if (kGated || b) v.b = *(reinterpret_cast<const uint4*>(b) + c);
+  v.a = v.b = make_uint4(0, 0, 0, 0);
+  if (in) v.a = *(reinterpret_cast<const uint4*>(a) + c);
+  if (in && two) v.b = *(reinterpret_cast<const uint4*>(b) + c);
   return v;
 }
 
 // Row values of chunk c as fp32; x + residual is written to h on the way.
 template <typename T, bool kGated>
-__device__ __forceinline__ void norm_combine(const NormParams& p, const NormRaw& v, const T* b,
-                                             T* h, int c, float (&f)[kVec<T>]) {
+__device__ __forceinline__ void norm_combine(const NormParams& p, const NormRaw& v, bool two, T* h,
+                                             int c, bool in, float (&f)[kVec<T>]) {
   constexpr int E = kVec<T>;
   Vec16<T> x, y;
   x.u = v.a;
@@ -98,23 +104,32 @@ __device__ __forceinline__ void norm_combine(const NormParams& p, const NormRaw&
 #pragma unroll
   for (int i = 0; i < E; ++i) f[i] = Elem<T>::to_float(x.e[i]);
   if constexpr (kGated) {
-    activate_exact_all(f, p.act);
+    if (in) {   // (a warp with nothing left skips the activation)
+      activate_exact_all(f, p.act);
 #pragma unroll
-    for (int i = 0; i < E; ++i) f[i] = __fmul_rn(f[i], Elem<T>::to_float(y.e[i]));
-  } else if (b) {
+      for (int i = 0; i < E; ++i) f[i] = __fmul_rn(f[i], Elem<T>::to_float(y.e[i]));
+    }
+  } else if (two) {
 #pragma unroll
-    for (int i = 0; i < E; ++i) f[i] = __fadd_rn(f[i], Elem<T>::to_float(y.e[i]));
-    store_vec(h + static_cast<int64_t>(c) * E, f);
+    for (int i = 0; i < E; ++i) {
+      x.e[i] = Elem<T>::from_float(__fadd_rn(f[i], Elem<T>::to_float(y.e[i])));
+      f[i] = Elem<T>::to_float(x.e[i]);
+    }
+    if (in) *(reinterpret_cast<uint4*>(h) + c) = x.u;
   }
 }
 
 // The weights of chunk c (ones without a weight): asked for before the row's
 // sum is exchanged, so that they are there when r is.
 template <int E>
-__device__ __forceinline__ void norm_weights(const float* w, int c, float4 (&to)[E / 4]) {
+__device__ __forceinline__ void norm_weights(const float* w, int c, bool in,
+                                             float4 (&to)[E / 4]) {
   const float4* w4 = reinterpret_cast<const float4*>(w) + static_cast<int64_t>(c) * (E / 4);
 #pragma unroll
-  for (int i = 0; i < E / 4; ++i) to[i] = __ldg(w4 + i);
+  for (int i = 0; i < E / 4; ++i) {
+    to[i] = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+    if (in) to[i] = __ldg(w4 + i);
+  }
 }
 
 template <int E>
@@ -176,12 +191,13 @@ __device__ __forceinline__ void norm_store_codes(int8_t* out, int first, int ste
 #pragma unroll
     for (int j = 0; j < R; ++j) {
       const int c = first + j * step;
-      if (c < end) {
-        uint32_t* o = reinterpret_cast<uint32_t*>(out + static_cast<int64_t>(c) * E);
-        if constexpr (E == 8)
-          *reinterpret_cast<uint2*>(o) = make_uint2(four(&v[j][0]), four(&v[j][4]));
-        else
-          o[0] = four(&v[j][0]);
+      uint32_t* o = reinterpret_cast<uint32_t*>(out + static_cast<int64_t>(c) * E);
+      if constexpr (E == 8) {
+        const uint2 w = make_uint2(four(&v[j][0]), four(&v[j][4]));
+        if (c < end) *reinterpret_cast<uint2*>(o) = w;
+      } else {
+        const uint32_t w = four(&v[j][0]);
+        if (c < end) o[0] = w;
       }
     }
   };
@@ -228,9 +244,10 @@ __device__ __forceinline__ V norm_exchange(NormExchange<V, W>& x, V v, int C, in
   if (C == 1) {
     if (lane == 0) x.slot[warp] = v;
     __syncthreads();
-    V s = x.slot[lane & (W - 1)];
+    constexpr int P = W <= 4 ? 4 : W <= 8 ? 8 : 16;   // W is 4, 5, 8 or 16
+    V s = (lane & (P - 1)) < W ? x.slot[lane & (P - 1)] : none;
 #pragma unroll
-    for (int o = W / 2; o > 0; o >>= 1) s = combine(s, __shfl_xor_sync(0xFFFFFFFFu, s, o));
+    for (int o = P / 2; o > 0; o >>= 1) s = combine(s, __shfl_xor_sync(0xFFFFFFFFu, s, o));
     return s;
   }
   if (lane < to) st_async(&x.slot[rank * W + warp], &x.full, lane, v);
@@ -250,17 +267,17 @@ __device__ __forceinline__ float norm_row_max(NormExchange<uint32_t, W>& x, floa
                                               int rank, int warp, int lane, int* abort,
                                               unsigned long long wait_ns) {
   const uint32_t top = norm_exchange<W>(
-      x, __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most) & 0x7FFFFFFFu), C, C, rank, warp, lane, abort, wait_ns,
-      0u, [](uint32_t a, uint32_t b) { return max(a, b); });
+      x, __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most) & 0x7FFFFFFFu), C, C, rank, warp,
+      lane, abort, wait_ns, 0u, [](uint32_t a, uint32_t b) { return max(a, b); });
   return __uint_as_float(top < 0x7F800000u ? top : 0x7FC00000u);
 }
 
 // One row per cluster; p.slice <= R * kThreads.
-template <typename T, int kThreads, bool kGated>
+template <typename T, int kThreads, int kElems, bool kGated>
 static __global__ void __launch_bounds__(kThreads)
 norm_quant_kernel(const __grid_constant__ NormParams p) {
   constexpr int E = kVec<T>;
-  constexpr int R = kNormRegElems / E;
+  constexpr int R = kElems / E;
   constexpr int W = kThreads / 32;
   __shared__ NormExchange<double, W> xd;
   __shared__ NormExchange<uint32_t, W> xm, xs;
@@ -292,37 +309,31 @@ norm_quant_kernel(const __grid_constant__ NormParams p) {
 
   // Everything is asked for before anything is used: a store to h between two
   // loads, or a choice of activation, would leave one load in flight at a time.
+  const bool two = kGated || b != nullptr;
   NormRaw raw[R];
 #pragma unroll
-  for (int j = 0; j < R; ++j) {
-    const int c = c0 + j * kThreads;
-    if (c < c1) raw[j] = norm_fetch<T, kGated>(a, b, c);
-  }
+  for (int j = 0; j < R; ++j)
+    raw[j] = norm_fetch(a, b, c0 + j * kThreads, c0 + j * kThreads < c1, two);
   float v[R][E];
 #pragma unroll
-  for (int j = 0; j < R; ++j) {
-    const int c = c0 + j * kThreads;
-    if (c < c1) norm_combine<T, kGated>(p, raw[j], b, h, c, v[j]);
-  }
+  for (int j = 0; j < R; ++j)
+    norm_combine<T, kGated>(p, raw[j], two, h, c0 + j * kThreads, c0 + j * kThreads < c1, v[j]);
   float r = 1.0f;
   float4 w[R][E / 4];
   if (p.weight) {
 #pragma unroll
     for (int j = 0; j < R; ++j)
-      if (c0 + j * kThreads < c1) norm_weights<E>(p.weight, c0 + j * kThreads, w[j]);
+      norm_weights<E>(p.weight, c0 + j * kThreads, c0 + j * kThreads < c1, w[j]);
   }
   if (p.normalize) {
     double ss[4] = {0.0, 0.0, 0.0, 0.0};   // four chains: the additions' latency
-    auto square = [&](const float (&f)[E]) {
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const double d = static_cast<double>(f[i]);
-        ss[i & 3] = fma(d, d, ss[i & 3]);
-      }
-    };
 #pragma unroll
     for (int j = 0; j < R; ++j)
-      if (c0 + j * kThreads < c1) square(v[j]);
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const double d = static_cast<double>(v[j][i]);
+        ss[i & 3] = fma(d, d, ss[i & 3]);
+      }
     double t = (ss[0] + ss[1]) + (ss[2] + ss[3]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
@@ -332,15 +343,14 @@ norm_quant_kernel(const __grid_constant__ NormParams p) {
   }
 
   float most = 0.0f;
+  if (p.normalize) {
 #pragma unroll
-  for (int j = 0; j < R; ++j) {
-    const int c = c0 + j * kThreads;
-    if (c < c1) {
-      if (p.normalize) norm_scale<E>(p.weight != nullptr, w[j], r, v[j]);
-#pragma unroll
-      for (int i = 0; i < E; ++i) most = norm_max(most, v[j][i]);
-    }
+    for (int j = 0; j < R; ++j) norm_scale<E>(p.weight != nullptr, w[j], r, v[j]);
   }
+#pragma unroll
+  for (int j = 0; j < R; ++j)
+#pragma unroll
+    for (int i = 0; i < E; ++i) most = norm_max(most, v[j][i]);
   const float amax = norm_row_max<W>(xm, most, C, rank, warp, lane, &abort, p.wait_ns);
   const NormScale q(amax);
   int sum = 0;
@@ -361,16 +371,16 @@ norm_quant_kernel(const __grid_constant__ NormParams p) {
   }
 }
 
-// Whole rows, K <= kNormRegElems * kThreads, in persistent CTAs.  The next row
+// Whole rows, K <= kElems * kThreads, in persistent CTAs.  The next row
 // of a CTA is on its way into shared memory (bulk copies) while the present
 // one, in registers, goes through its sum and its maximum, so memory does not
-// wait for the reductions (2048 x 8192 fp32 with a residual: 38.4 us against
+// wait for the reductions (2048 x 8192 fp32 with a residual: 37.6 us against
 // 62.8 with one CTA per row and no copy ahead).
-template <typename T, int kThreads, bool kGated>
+template <typename T, int kThreads, int kElems, bool kGated>
 static __global__ void __launch_bounds__(kThreads)
 norm_stream_kernel(const __grid_constant__ NormParams p, int rows) {
   constexpr int E = kVec<T>;
-  constexpr int R = kNormRegElems / E;
+  constexpr int R = kElems / E;
   constexpr int W = kThreads / 32;
   extern __shared__ __align__(128) uint8_t next_row[];   // x or gate, then residual or up
   __shared__ NormExchange<double, W> xd;
@@ -404,12 +414,9 @@ norm_stream_kernel(const __grid_constant__ NormParams p, int rows) {
 #pragma unroll
     for (int j = 0; j < R; ++j) {
       const int c = tid + j * kThreads;
-      if (c < C) {
-        NormRaw raw;
-        raw.a = reinterpret_cast<const uint4*>(next_row)[c];
-        if (two) raw.b = reinterpret_cast<const uint4*>(next_row + bytes)[c];
-        norm_combine<T, kGated>(p, raw, two ? static_cast<const T*>(p.b) : nullptr, h, c, v[j]);
-      }
+      const NormRaw raw = norm_fetch(reinterpret_cast<const T*>(next_row),
+                                     reinterpret_cast<const T*>(next_row + bytes), c, c < C, two);
+      norm_combine<T, kGated>(p, raw, two, h, c, c < C, v[j]);
     }
     if (!__syncthreads_and(ok)) break;             // the row has been read, by all
     fetched = row + gridDim.x < rows;
@@ -420,18 +427,16 @@ norm_stream_kernel(const __grid_constant__ NormParams p, int rows) {
     if (p.weight) {
 #pragma unroll
       for (int j = 0; j < R; ++j)
-        if (tid + j * kThreads < C) norm_weights<E>(p.weight, tid + j * kThreads, w[j]);
+        norm_weights<E>(p.weight, tid + j * kThreads, tid + j * kThreads < C, w[j]);
     }
     if (p.normalize) {
       double ss[4] = {0.0, 0.0, 0.0, 0.0};
 #pragma unroll
       for (int j = 0; j < R; ++j)
-        if (tid + j * kThreads < C) {
 #pragma unroll
-          for (int i = 0; i < E; ++i) {
-            const double d = static_cast<double>(v[j][i]);
-            ss[i & 3] = fma(d, d, ss[i & 3]);
-          }
+        for (int i = 0; i < E; ++i) {
+          const double d = static_cast<double>(v[j][i]);
+          ss[i & 3] = fma(d, d, ss[i & 3]);
         }
       double t = (ss[0] + ss[1]) + (ss[2] + ss[3]);
 #pragma unroll
@@ -441,13 +446,14 @@ norm_stream_kernel(const __grid_constant__ NormParams p, int rows) {
       r = norm_rsqrt(fma(t, p.inv_k, p.eps));
     }
     float most = 0.0f;
+    if (p.normalize) {
+#pragma unroll
+      for (int j = 0; j < R; ++j) norm_scale<E>(p.weight != nullptr, w[j], r, v[j]);
+    }
 #pragma unroll
     for (int j = 0; j < R; ++j)
-      if (tid + j * kThreads < C) {
-        if (p.normalize) norm_scale<E>(p.weight != nullptr, w[j], r, v[j]);
 #pragma unroll
-        for (int i = 0; i < E; ++i) most = norm_max(most, v[j][i]);
-      }
+      for (int i = 0; i < E; ++i) most = norm_max(most, v[j][i]);
     const float amax = norm_row_max<W>(xm, most, 1, 0, warp, lane, &abort, p.wait_ns);
     const NormScale q(amax);
     int8_t* out = p.xq + row * p.K;

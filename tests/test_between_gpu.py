@@ -70,6 +70,33 @@ def test_norm_quant(N, K, dtype):
     check_codes(got, ref.norm_rows(f32(h), w.cpu().numpy(), EPS))
 
 
+# each register count of the kernels at its limit and just past it, in several
+# rounds of the resident CTAs (a row's padding does not reach the next row)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("K", [1008, 1024, 1040, 2032, 2048, 2064, 2544, 2560, 2576, 4080, 4096,
+                               6128, 6144, 6160, 12272, 12288, 12304, 65536, 65552])
+def test_norm_quant_at_each_register_count(K, dtype):
+    N = 2500 if K <= 2576 else 700 if K <= 12304 else 3
+    x, res, w = rows(N, K, K, dtype), rows(N, K, K + 1, dtype, scale=3.0), weight(K, K)
+    x[1::7] = 0.0
+    x[2::11, K - 1] = float("inf")
+    pick = torch.cat([torch.arange(0, min(N, 12)), torch.arange(max(N - 12, 0), N)]).unique().cuda()
+    h, *got = api.norm_quant(x, w, eps=EPS, residual=res)
+    assert torch.equal(h, (x.float() + res.float()).to(dtype))
+    check_codes([g[pick] for g in got], ref.norm_rows(f32(h[pick]), w.cpu().numpy(), EPS))
+    # the rows in another order: every row's codes follow it
+    back = torch.arange(N - 1, -1, -1, device="cuda")
+    again = api.norm_quant(h[back].contiguous(), w, eps=EPS)
+    for g, o in zip(got, again):
+        assert torch.equal(g[back].nan_to_num(-1.0) if g.is_floating_point() else g[back],
+                           o.nan_to_num(-1.0) if o.is_floating_point() else o)
+    gated = api.gated_norm_quant(x, res, w, activation="relu2", eps=EPS)
+    a = np.maximum(f32(x[pick]), np.float32(0))
+    with np.errstate(all="ignore"):
+        v = a * a * f32(res[pick])
+    check_codes([g[pick] for g in gated], ref.norm_rows(v, w.cpu().numpy(), EPS))
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("N,K,pad", [(1, 144, 16), (9, 2000, 48), (4, 40000, 80)])
 def test_norm_quant_strided_and_in_place(N, K, pad, dtype):
