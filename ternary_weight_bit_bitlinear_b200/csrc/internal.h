@@ -46,7 +46,7 @@ struct DeviceInfo {
   bool gemv_split_attr_set[bl::kGemvMaxTokens + 1] = {};
   int gemv_ep_blocks_per_sm[bl::kGemvEpMaxTokens + 1] = {};     // 0: not set up yet
   bool gemv_ep_split_attr_set[bl::kGemvEpMaxTokens + 1] = {};
-  NormKernelInfo norm[3][2][8];       // type, gated, width (launch_norm.cu)
+  NormKernelInfo norm[3][2][9];       // type, gated, width (launch_norm.cu)
   bool split_attr_set[3] = {};        // gemm_split_kernel: 32, 64, 128 tokens
   int split_clusters[3][3] = {};      // resident clusters of 1, 2, 4 pairs; 0: not asked yet
 };

@@ -76,6 +76,12 @@ bitlinear_status launch_cluster(int64_t rows, int C, bl::NormParams p, cudaStrea
 // threads 14.6 / 17.7 / 29.7 us), with few registers a thread past the row's
 // end (their zeros run through all of the arithmetic: 2048 x 2560 bf16 in
 // 160 threads of 16 values 10.2 us, in 128 of 32 12.2; 512 rows 4.7 and 5.6).
+// Up to 12288 elements of 16 bits, where instructions bound it, two CTAs of 256
+// threads with 48 values each go through their reductions in turn, against one
+// of 512 with 24 (gate and up 512 x 11008: 11.3 and 13.5 us, 2048: 30.6 and
+// 39.8); one row for an SM (64: 7.5 and 5.9) and fp32 (2048: 51.5 and 49.0)
+// take the wide one.  The same trade at other widths: no gain at 2048 rows of
+// 5120 to 8192, 1.1 times the time at 14336 and 16384 (64 values).
 // From 16384 elements on that would be 1024 threads of 64 registers, which
 // spill: clusters there, of 8 CTAs while the rows leave SMs idle (one row of
 // 28672: 4.0 us; 256 rows: 31 with 4 x 256 threads, 49 with 8 x 512), and
@@ -91,6 +97,10 @@ bitlinear_status launch_norm_type(int rows, const bl::NormParams& p, DeviceInfo*
   if (K <= 4096) return launch_stream<T, 128, 32, kGated>(rows, p, known[3], sms, s);
   if (K <= 6144) return launch_stream<T, 256, 24, kGated>(rows, p, known[4], sms, s);
   if (K <= 8192) return launch_stream<T, 256, 32, kGated>(rows, p, known[5], sms, s);
+  if constexpr (sizeof(T) == 2) {
+    if (K <= 12288 && rows > sms)
+      return launch_stream<T, 256, 48, kGated>(rows, p, known[8], sms, s);
+  }
   if (K <= 12288) return launch_stream<T, 512, 24, kGated>(rows, p, known[6], sms, s);
   if (K <= 16384) return launch_stream<T, 512, 32, kGated>(rows, p, known[7], sms, s);
   if (K <= 32768 && rows * int64_t(8) > sms)

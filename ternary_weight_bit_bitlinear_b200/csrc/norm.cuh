@@ -15,7 +15,7 @@
 // NaN: a row that holds either gets amax = NaN and q = 0.
 //
 // Two kernels, both reading each element once and holding it in registers from
-// the load to the codes (kElems per thread, 8 to 32):
+// the load to the codes (kElems per thread, 8 to 48):
 //   norm_stream_kernel  rows up to 16384 wide, one CTA per row: persistent CTAs
 //                       whose next row is on its way into shared memory while
 //                       the present one goes through its sum and its maximum;

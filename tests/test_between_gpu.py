@@ -74,7 +74,7 @@ def test_norm_quant(N, K, dtype):
 # rounds of the resident CTAs (a row's padding does not reach the next row)
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("K", [1008, 1024, 1040, 2032, 2048, 2064, 2544, 2560, 2576, 4080, 4096,
-                               6128, 6144, 6160, 12272, 12288, 12304, 65536, 65552])
+                               6128, 6144, 6160, 8192, 8208, 12272, 12288, 12304, 65536, 65552])
 def test_norm_quant_at_each_register_count(K, dtype):
     N = 2500 if K <= 2576 else 700 if K <= 12304 else 3
     x, res, w = rows(N, K, K, dtype), rows(N, K, K + 1, dtype, scale=3.0), weight(K, K)
