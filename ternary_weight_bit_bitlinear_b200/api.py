@@ -1,9 +1,9 @@
 """Torch-facing calls of the ternary BitLinear path.
 
 Each function checks dtype, device and contiguity, allocates its outputs with
-torch (device memory is torch's job here), and hands raw pointers to one C
-entry point of libbitlinear.so.  All arithmetic runs in the CUDA kernels;
-nothing here falls back to the CPU.
+torch (device memory is torch's job here) from the pool of the stream that
+writes them, and hands raw pointers to one C entry point of libbitlinear.so.
+All arithmetic runs in the CUDA kernels; nothing here falls back to the CPU.
 """
 import torch
 
@@ -42,6 +42,27 @@ def _on(device, **tensors):
                              "device" % (name, t.device, device))
 
 
+def _allocate(stream, like, *shapes):
+    """Uninitialised tensors beside `like`, (shape, dtype) each, that belong to
+    the stream that will write them: nothing pending elsewhere still uses their
+    memory, and once dropped it is not handed out again before that stream is
+    done with it.  Outputs, codes and workspaces all come from here."""
+    if stream is None:
+        return [like.new_empty(s, dtype=d) for s, d in shapes]
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        stream = torch.cuda.ExternalStream(handle, device=like.device)
+    with torch.cuda.stream(stream):
+        return [like.new_empty(s, dtype=d) for s, d in shapes]
+
+
+def _outputs(stream, like, N, M, out, with_acc):
+    """y (`out` where it is given) and acc (None unless asked for) of a product."""
+    if out is None:
+        out, = _allocate(stream, like, ((N, M), torch.float32))
+    return out, (_allocate(stream, like, ((N, M), torch.int32))[0] if with_acc else None)
+
+
 def _check_out(out, N, M, device, name="out"):
     """A caller-supplied output must be fp32 [N, M], contiguous, on `device`
     (the kernels write N*M floats through its pointer)."""
@@ -72,10 +93,9 @@ def pack_weights(W, stream=None):
     words, alpha fp32 [1])."""
     _need(W, torch.float32, "W")
     M, K = W.shape
-    packed = torch.empty((M, packed_row_words(K)), dtype=torch.int32, device=W.device)
-    alpha = torch.empty(1, dtype=torch.float32, device=W.device)
     nbytes = _lib.bitlinear_pack_workspace_bytes(M, K)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=W.device)
+    packed, alpha, ws = _allocate(stream, W, ((M, packed_row_words(K)), torch.int32),
+                                  (1, torch.float32), (nbytes, torch.uint8))
     _lib.check(_lib.bitlinear_pack_weights(W, M, K, packed, alpha, ws, nbytes, stream),
                "bitlinear_pack_weights")
     return packed, alpha
@@ -85,9 +105,9 @@ def quant_act(x, stream=None, with_sum=True):
     """fp32 x[N,K] -> (xq int8 [N,K], amax fp32 [N], xsum int32 [N] or None)."""
     _need(x, torch.float32, "x")
     N, K = x.shape
-    xq = torch.empty((N, K), dtype=torch.int8, device=x.device)
-    amax = torch.empty(N, dtype=torch.float32, device=x.device)
-    xsum = torch.empty(N, dtype=torch.int32, device=x.device) if with_sum else None
+    xq, amax, *xsum = _allocate(stream, x, ((N, K), torch.int8), (N, torch.float32),
+                                *(((N, torch.int32),) if with_sum else ()))
+    xsum = xsum[0] if with_sum else None
     _lib.check(_lib.bitlinear_quant_act(x, N, K, xq, amax, xsum, stream), "bitlinear_quant_act")
     return xq, amax, xsum
 
@@ -96,11 +116,9 @@ def quant_act_per_tensor(x, stream=None):
     """Per-tensor variant: one absmax over all of x; amax[n] holds it for every n."""
     _need(x, torch.float32, "x")
     N, K = x.shape
-    xq = torch.empty((N, K), dtype=torch.int8, device=x.device)
-    amax = torch.empty(N, dtype=torch.float32, device=x.device)
-    xsum = torch.empty(N, dtype=torch.int32, device=x.device)
     nbytes = _lib.load().bitlinear_quant_act_per_tensor_workspace_bytes()
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+    xq, amax, xsum, ws = _allocate(stream, x, ((N, K), torch.int8), (N, torch.float32),
+                                   (N, torch.int32), (nbytes, torch.uint8))
     _lib.check(_lib.bitlinear_quant_act_per_tensor(x, N, K, xq, amax, xsum, ws, nbytes, stream),
                "bitlinear_quant_act_per_tensor")
     return xq, amax, xsum
@@ -113,9 +131,8 @@ def quant_act_grouped(xs, stream=None):
     for x in xs:
         _need(x, torch.float32, "x")
         N, K = x.shape
-        o = (torch.empty((N, K), dtype=torch.int8, device=x.device),
-             torch.empty(N, dtype=torch.float32, device=x.device),
-             torch.empty(N, dtype=torch.int32, device=x.device))
+        o = tuple(_allocate(stream, x, ((N, K), torch.int8), (N, torch.float32),
+                            (N, torch.int32)))
         outs.append(o)
         entries.append((x,) + o)
     arr = _lib.make_acts(entries)
@@ -137,8 +154,7 @@ def _matmul(fn, name, packed, alpha, xq, amax, xsum, M, with_acc, stream, out=No
     dev = packed.device
     _on(dev, alpha=alpha, xq=xq, amax=amax, xsum=xsum)
     _check_out(out, N, M, dev)
-    y = out if out is not None else torch.empty((N, M), dtype=torch.float32, device=dev)
-    acc = torch.empty((N, M), dtype=torch.int32, device=dev) if with_acc else None
+    y, acc = _outputs(stream, packed, N, M, out, with_acc)
     with torch.cuda.device(dev):
         _lib.check(fn(packed, alpha, M, K, xq, amax, xsum, N, y, acc, stream), name)
     return (y, acc) if with_acc else y
@@ -174,9 +190,7 @@ def _grouped(fn, name, layers, xq, amax, xsum, with_acc, stream, outs):
         _on(dev, packed=packed, alpha=alpha, xq=xqs[i], amax=amaxs[i], xsum=xsums[i])
         if outs is not None:
             _check_out(outs[i], N, M, dev, "outs[%d]" % i)
-        y = outs[i] if outs is not None else torch.empty((N, M), dtype=torch.float32,
-                                                           device=dev)
-        acc = torch.empty((N, M), dtype=torch.int32, device=dev) if with_acc else None
+        y, acc = _outputs(stream, packed, N, M, None if outs is None else outs[i], with_acc)
         ys.append(y)
         accs.append(acc)
         entries.append((packed, alpha, M, K, xqs[i], amaxs[i], xsums[i], y, acc))
@@ -246,8 +260,7 @@ def gemv_quant(packed, alpha, x, M=None, with_acc=False, stream=None, out=None):
     dev = packed.device
     _on(dev, alpha=alpha, x=x)
     _check_out(out, N, M, dev)
-    y = out if out is not None else torch.empty((N, M), dtype=torch.float32, device=dev)
-    acc = torch.empty((N, M), dtype=torch.int32, device=dev) if with_acc else None
+    y, acc = _outputs(stream, packed, N, M, out, with_acc)
     with torch.cuda.device(dev):
         _lib.check(_lib.bitlinear_gemv_quant(packed, alpha, M, K, x, N, y, acc, stream),
                    "bitlinear_gemv_quant")
@@ -278,9 +291,7 @@ def gemv_quant_grouped(layers, x, with_acc=False, stream=None, outs=None):
         _on(dev, packed=packed, alpha=alpha, x=xs[i])
         if outs is not None:
             _check_out(outs[i], N, M, dev, "outs[%d]" % i)
-        y = outs[i] if outs is not None else torch.empty((N, M), dtype=torch.float32,
-                                                           device=dev)
-        acc = torch.empty((N, M), dtype=torch.int32, device=dev) if with_acc else None
+        y, acc = _outputs(stream, packed, N, M, None if outs is None else outs[i], with_acc)
         ys.append(y)
         accs.append(acc)
         entries.append((packed, alpha, M, K, xs[i], y, acc))
@@ -307,7 +318,7 @@ def tl2_from_packed(packed, K, stream=None):
     M = packed.shape[0]
     if packed.shape[1] != packed_row_words(K):
         raise ValueError("packed must be [M, packed_row_words(K)]")
-    out = torch.empty((M, tl2_row_bytes(K)), dtype=torch.uint8, device=packed.device)
+    out, = _allocate(stream, packed, ((M, tl2_row_bytes(K)), torch.uint8))
     _lib.check(_lib.bitlinear_tl2_from_packed(packed, M, K, out, stream),
                "bitlinear_tl2_from_packed")
     return out
@@ -326,8 +337,7 @@ def gemv_tl2(tl2, alpha, xq, amax, M=None, with_acc=False, stream=None, out=None
     dev = tl2.device
     _on(dev, alpha=alpha, xq=xq, amax=amax)
     _check_out(out, N, M, dev)
-    y = out if out is not None else torch.empty((N, M), dtype=torch.float32, device=dev)
-    acc = torch.empty((N, M), dtype=torch.int32, device=dev) if with_acc else None
+    y, acc = _outputs(stream, tl2, N, M, out, with_acc)
     with torch.cuda.device(dev):
         _lib.check(_lib.bitlinear_gemv_tl2(tl2, alpha, M, K, xq, amax, N, y, acc, stream),
                    "bitlinear_gemv_tl2")
@@ -402,18 +412,6 @@ def _launch(fn, name, dev, stream, *args):
         status = fn(*args, _lib.raw_stream(stream, dev.index))
     if status != _lib.OK:
         raise _lib.BitLinearError(status, name)
-
-
-def _allocate(stream, like, *shapes):
-    """Uninitialised tensors beside `like`, (shape, dtype) each, that belong to
-    the stream that will write them, so that their memory is not handed out
-    again before that."""
-    if stream is None:
-        return [like.new_empty(s, dtype=d) for s, d in shapes]
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
-    with torch.cuda.stream(stream):
-        return [like.new_empty(s, dtype=d) for s, d in shapes]
 
 
 def norm_quant(x, weight=None, eps=1e-5, residual=None, normalize=True, h_out=None, stream=None):

@@ -1,0 +1,142 @@
+"""Which stream the torch-facing calls allocate on, on the CPU.
+
+A call that is given a stream writes its outputs, its int8 codes and its
+workspace there.  Their memory has to come from that stream's pool: memory of
+the current stream's pool may still be in use by work pending there when the
+call writes it, and a temporary goes back to the pool when the call returns,
+before its stream has run.  Here the C entry points, the device and stream
+contexts and torch's allocating calls are replaced by recorders.
+"""
+import contextlib
+
+import pytest
+import torch
+
+from ternary_weight_bit_bitlinear_b200 import _lib, api, build
+
+DEV = torch.device("cpu")
+
+
+class Stream:
+    cuda_stream = 0x51
+
+
+class Record:
+    """Active streams and devices, and what was active at each allocation and
+    at each call of an entry point."""
+
+    def __init__(self):
+        self.streams, self.devices = [], []
+        self.allocated, self.called = [], []
+
+    @contextlib.contextmanager
+    def stream(self, s):
+        self.streams.append(s.cuda_stream)
+        yield
+        self.streams.pop()
+
+    @contextlib.contextmanager
+    def device(self, d):
+        self.devices.append(torch.device(d))
+        yield
+        self.devices.pop()
+
+
+@pytest.fixture
+def record(monkeypatch):
+    build.build()
+    _lib.load()
+    r = Record()
+
+    def external(handle, device=None):
+        s = Stream()
+        s.cuda_stream = handle
+        return s
+
+    def noting(fn):
+        def f(*a, **kw):
+            r.allocated.append(r.streams[-1] if r.streams else None)
+            return fn(*a, **kw)
+        return f
+
+    def entry(name):
+        def f(*a):
+            r.called.append((name, r.devices[-1] if r.devices else None))
+            return _lib.OK
+        return f
+
+    monkeypatch.setattr(api, "_need", lambda *a: None)
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", external)
+    monkeypatch.setattr(torch.cuda, "stream", r.stream)
+    monkeypatch.setattr(torch.cuda, "device", r.device)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)   # never the tensors' own
+    monkeypatch.setattr(torch, "empty", noting(torch.empty))
+    monkeypatch.setattr(torch.Tensor, "new_empty", noting(torch.Tensor.new_empty))
+    for name in [n for n in dir(_lib) if n.startswith("bitlinear_") and n not in
+                 ("bitlinear_pack_workspace_bytes",)]:
+        monkeypatch.setattr(_lib, name, entry(name))
+    lib = _lib.load()
+
+    class Calls:      # the loaded library, its launching entry points replaced
+        bitlinear_linear = staticmethod(entry("bitlinear_linear"))
+
+        def __getattr__(self, name):
+            return getattr(lib, name)
+    monkeypatch.setattr(_lib, "load", lambda *a: Calls())
+    monkeypatch.setattr(_lib, "raw_stream", lambda s, i: getattr(s, "cuda_stream", s) or 0)
+    return r
+
+
+def layer(bias):
+    packed = torch.zeros((96, api.packed_row_words(160)), dtype=torch.int32)
+    return api.TernaryLinear(packed, torch.ones(1), 160, 96, torch.zeros(96) if bias else None)
+
+
+def codes(N, K=160):
+    return (torch.zeros((N, K), dtype=torch.int8), torch.zeros(N),
+            torch.zeros(N, dtype=torch.int32))
+
+
+CALLS = {
+    "layer, one token": lambda s: layer(False)(torch.zeros(1, 160), stream=s),
+    "layer, six tokens": lambda s: layer(False)(torch.zeros(6, 160), stream=s),
+    "layer with a bias": lambda s: layer(True)(torch.zeros(6, 160), stream=s),
+    "layer, its codes given": lambda s: layer(True).quantized(*codes(6), stream=s),
+    "pack_weights": lambda s: api.pack_weights(torch.zeros(96, 160), s),
+    "quant_act": lambda s: api.quant_act(torch.zeros(6, 160), s),
+    "quant_act_grouped": lambda s: api.quant_act_grouped([torch.zeros(6, 160)] * 2, s),
+    "quant_act_per_tensor": lambda s: api.quant_act_per_tensor(torch.zeros(6, 160), s),
+    "gemv": lambda s: api.gemv(layer(False).packed, torch.ones(1), *codes(2), with_acc=True,
+                               stream=s),
+    "gemm": lambda s: api.gemm(layer(False).packed, torch.ones(1), *codes(2), stream=s),
+    "gemv_quant": lambda s: api.gemv_quant(layer(False).packed, torch.ones(1),
+                                           torch.zeros(2, 160), with_acc=True, stream=s),
+    "gemm_grouped": lambda s: api.gemm_grouped([(layer(False).packed, torch.ones(1))] * 2,
+                                               *codes(2), with_acc=True, stream=s),
+    "gemv_quant_grouped": lambda s: api.gemv_quant_grouped(
+        [(layer(False).packed, torch.ones(1))] * 2, torch.zeros(2, 160), with_acc=True, stream=s),
+    "tl2_from_packed": lambda s: api.tl2_from_packed(layer(False).packed, 160, s),
+    "gemv_tl2": lambda s: api.gemv_tl2(torch.zeros((96, api.tl2_row_bytes(160)),
+                                                   dtype=torch.uint8),
+                                       torch.ones(1), *codes(2)[:2], with_acc=True, stream=s),
+}
+
+
+@pytest.mark.parametrize("name", sorted(CALLS))
+def test_memory_of_a_call_belongs_to_its_stream(record, name):
+    class Other:                                        # another library's stream
+        cuda_stream = 0x99
+    for given in (Stream(), 0x77, Other()):             # 0x77: a raw handle
+        record.allocated.clear()
+        record.called.clear()
+        CALLS[name](given)
+        want = getattr(given, "cuda_stream", given)
+        assert record.called and record.allocated
+        assert all(s == want for s in record.allocated), (record.allocated, want)
+
+
+@pytest.mark.parametrize("name", sorted(CALLS))
+def test_without_a_stream_nothing_changes_the_current_one(record, name):
+    CALLS[name](None)
+    assert record.called and record.allocated and set(record.allocated) == {None}
