@@ -457,8 +457,12 @@ typedef struct {
  * The ternary product with its epilogue, over a list of layers that share the
  * token count (as bitlinear_gemm_grouped does):
  *   y[n,m] = act(acc[n,m] * (alpha * (amax[n]/127)) + bias[m]) + residual[n,m]
- * in fp32, rounded once to dtype; the divisions of silu and gelu_tanh are
- * within 2 units in the last place.  Any N: a few tokens run on the CUDA cores,
+ * in fp32, rounded once to dtype.  silu and gelu_tanh are evaluated as
+ * v e^t / (1 + e^t) for t < 0 and v / (1 + e^-t) elsewhere (t = v, or 2 sqrt(2/pi)
+ * (v + 0.044715 v^3)), so that they hold however far below zero v is; their
+ * quotient is within one unit in the last place of fp32, or within 2 where dtype
+ * has 16 bits.  v = -inf gives NaN in silu, gelu and gelu_tanh, as the formulas
+ * above do.  Any N: a few tokens run on the CUDA cores,
  * more on the tensor cores.  The layers of a call do not wait for one another.
  * y may be the residual itself (same pointer and stride); any other overlap is
  * an error of the caller.

@@ -3,8 +3,8 @@
 //
 //   y[n, m] = T(act(acc * (alpha * (amax[n] / 127)) + bias[m]) + residual[n, m])
 //
-// Every fp32 operation is rounded on its own; silu and gelu_tanh divide
-// approximately (activate_product).
+// Every fp32 operation is rounded on its own; the tensor-core kernels divide
+// approximately in silu and gelu_tanh of a 16-bit output (activate_product).
 #pragma once
 
 #include "element.cuh"
@@ -40,7 +40,7 @@ __device__ __forceinline__ void ep_store(void* p, int64_t o, int dtype, float v)
 // Element (n, m) from its rescaled accumulator v.
 __device__ __forceinline__ void ep_element(const Epilogue& e, int64_t n, int m, float v) {
   if (e.bias) v = __fadd_rn(v, __ldg(e.bias + m));
-  v = activate_product(v, e.act);
+  v = activate_product<true>(v, e.act);   // one form for all types: less code in a short launch
   if (e.residual) v = __fadd_rn(v, ep_load(e.residual, n * e.ldr + m, e.dtype));
   ep_store(e.y, n * e.ldy + m, e.dtype, v);
 }
@@ -123,7 +123,7 @@ struct EpRows {
 #pragma unroll
             for (int q = 0; q < E; ++q) f[q] = __fadd_rn(f[q], bias[q]);
           }
-          activate_all(f, e.act);
+          activate_all<T>(f, e.act);
           Vec16<T> v;
           v.u = res[i];
 #pragma unroll
@@ -152,7 +152,7 @@ struct EpRows {
         }
         if (e.bias) f[j] = __fadd_rn(f[j], bias[0]);
       }
-      activate_all(f, e.act);
+      activate_all<T>(f, e.act);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         if (j0 + j < nt) *y = Elem<T>::from_float(e.residual ? __fadd_rn(f[j], g[j]) : f[j]);
