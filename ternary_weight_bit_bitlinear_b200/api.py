@@ -42,6 +42,18 @@ def _on(device, **tensors):
                              "device" % (name, t.device, device))
 
 
+def _launch(fn, name, dev, stream, *args):
+    """fn(*args, raw stream) with `dev` current, whichever device was; raises on a
+    status other than OK."""
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            status = fn(*args, _lib.raw_stream(stream, dev.index))
+    else:
+        status = fn(*args, _lib.raw_stream(stream, dev.index))
+    if status != _lib.OK:
+        raise _lib.BitLinearError(status, name)
+
+
 def _allocate(stream, like, *shapes):
     """Uninitialised tensors beside `like`, (shape, dtype) each, that belong to
     the stream that will write them: nothing pending elsewhere still uses their
@@ -96,8 +108,8 @@ def pack_weights(W, stream=None):
     nbytes = _lib.bitlinear_pack_workspace_bytes(M, K)
     packed, alpha, ws = _allocate(stream, W, ((M, packed_row_words(K)), torch.int32),
                                   (1, torch.float32), (nbytes, torch.uint8))
-    _lib.check(_lib.bitlinear_pack_weights(W, M, K, packed, alpha, ws, nbytes, stream),
-               "bitlinear_pack_weights")
+    _launch(_lib.bitlinear_pack_weights, "bitlinear_pack_weights", W.device, stream,
+            W, M, K, packed, alpha, ws, nbytes)
     return packed, alpha
 
 
@@ -108,7 +120,8 @@ def quant_act(x, stream=None, with_sum=True):
     xq, amax, *xsum = _allocate(stream, x, ((N, K), torch.int8), (N, torch.float32),
                                 *(((N, torch.int32),) if with_sum else ()))
     xsum = xsum[0] if with_sum else None
-    _lib.check(_lib.bitlinear_quant_act(x, N, K, xq, amax, xsum, stream), "bitlinear_quant_act")
+    _launch(_lib.bitlinear_quant_act, "bitlinear_quant_act", x.device, stream,
+            x, N, K, xq, amax, xsum)
     return xq, amax, xsum
 
 
@@ -119,25 +132,28 @@ def quant_act_per_tensor(x, stream=None):
     nbytes = _lib.load().bitlinear_quant_act_per_tensor_workspace_bytes()
     xq, amax, xsum, ws = _allocate(stream, x, ((N, K), torch.int8), (N, torch.float32),
                                    (N, torch.int32), (nbytes, torch.uint8))
-    _lib.check(_lib.bitlinear_quant_act_per_tensor(x, N, K, xq, amax, xsum, ws, nbytes, stream),
-               "bitlinear_quant_act_per_tensor")
+    _launch(_lib.bitlinear_quant_act_per_tensor, "bitlinear_quant_act_per_tensor", x.device,
+            stream, x, N, K, xq, amax, xsum, ws, nbytes)
     return xq, amax, xsum
 
 
 def quant_act_grouped(xs, stream=None):
     """Quantise several fp32 activation matrices in one launch; returns a list
     of (xq, amax, xsum)."""
+    xs = list(xs)
     outs, entries = [], []
     for x in xs:
         _need(x, torch.float32, "x")
+        if x.device != xs[0].device:
+            raise ValueError("all activations of a call must share one device")
         N, K = x.shape
         o = tuple(_allocate(stream, x, ((N, K), torch.int8), (N, torch.float32),
                             (N, torch.int32)))
         outs.append(o)
         entries.append((x,) + o)
-    arr = _lib.make_acts(entries)
-    _lib.check(_lib.bitlinear_quant_act_grouped(arr, len(entries), stream),
-               "bitlinear_quant_act_grouped")
+    if entries:
+        _launch(_lib.bitlinear_quant_act_grouped, "bitlinear_quant_act_grouped", xs[0].device,
+                stream, _lib.make_acts(entries), len(entries))
     return outs
 
 
@@ -319,8 +335,8 @@ def tl2_from_packed(packed, K, stream=None):
     if packed.shape[1] != packed_row_words(K):
         raise ValueError("packed must be [M, packed_row_words(K)]")
     out, = _allocate(stream, packed, ((M, tl2_row_bytes(K)), torch.uint8))
-    _lib.check(_lib.bitlinear_tl2_from_packed(packed, M, K, out, stream),
-               "bitlinear_tl2_from_packed")
+    _launch(_lib.bitlinear_tl2_from_packed, "bitlinear_tl2_from_packed", packed.device, stream,
+            packed, M, K, out)
     return out
 
 
@@ -401,17 +417,6 @@ def _vector_ptr(t, n, dtype, name, device):
             raise ValueError("%s must hold %d entries, got %d" % (name, n, t.numel()))
         _on(device, **{name: t})
     return t.data_ptr()
-
-
-def _launch(fn, name, dev, stream, *args):
-    """fn(*args, raw stream) with `dev` current; raises on a status other than OK."""
-    if torch.cuda.current_device() != dev.index:
-        with torch.cuda.device(dev):
-            status = fn(*args, _lib.raw_stream(stream, dev.index))
-    else:
-        status = fn(*args, _lib.raw_stream(stream, dev.index))
-    if status != _lib.OK:
-        raise _lib.BitLinearError(status, name)
 
 
 def norm_quant(x, weight=None, eps=1e-5, residual=None, normalize=True, h_out=None, stream=None):

@@ -140,3 +140,11 @@ def test_memory_of_a_call_belongs_to_its_stream(record, name):
 def test_without_a_stream_nothing_changes_the_current_one(record, name):
     CALLS[name](None)
     assert record.called and record.allocated and set(record.allocated) == {None}
+
+
+@pytest.mark.parametrize("name", sorted(CALLS))
+def test_calls_launch_with_the_device_of_their_tensors_current(record, name):
+    """Another device may be current: the pointers are of the tensors' own."""
+    for given in (None, Stream()):
+        CALLS[name](given)
+    assert record.called and all(d == DEV for _, d in record.called), record.called
