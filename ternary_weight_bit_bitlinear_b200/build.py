@@ -27,7 +27,7 @@ NVCC_FLAGS = [
 
 def sources():
     return [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC))
-            if f.endswith((".cu", ".cuh"))] + [os.path.join(INCLUDE, "bitlinear.h")]
+            if f.endswith((".cu", ".cuh", ".h"))] + [os.path.join(INCLUDE, "bitlinear.h")]
 
 
 def units():

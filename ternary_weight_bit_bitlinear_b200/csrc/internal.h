@@ -19,6 +19,7 @@
 #include "gemm_split.cuh"
 #include "gemv.cuh"
 #include "gemv_quant.cuh"
+#include "launch_facts.h"
 #include "norm.cuh"
 #include "tl2.cuh"
 
@@ -29,26 +30,25 @@ constexpr int kMaxDevices = 64;
 // A row kernel of norm.cuh: set up, and its CTAs per SM at the last
 // shared-memory size asked about.
 struct NormKernelInfo {
-  bool set = false;
-  int smem = 0, per_sm = 0;
+  FlagFact set{false};
+  KeyedFact per_sm;   // by bytes of shared memory
 };
 
-// Per-device facts and one-time set-up flags, looked up once per device.
+// Per-device facts and one-time set-up flags, looked up once per device, by any
+// host thread (launch_facts.h).
 struct DeviceInfo {
   int sms = 0;
-  bool gemm_attr_set[8] = {};
-  int gemv_blocks_per_sm[bl::kGemvMaxTokens + 1] = {};   // 0: not set up yet
-  int tl2_blocks_per_sm[bl::kGemvMaxTokens + 1] = {};    // 0: not set up yet
-  bool gq_attr_set[bl::kGemvMaxTokens + 1] = {};
-  int gq_max_dyn[bl::kGemvMaxTokens + 1] = {};            // dynamic shared memory limit
-  int gq_area[bl::kGemvMaxTokens + 1][bl::kGqMaxWarps + 1] = {};   // last shared-memory size
-  int gq_occ[bl::kGemvMaxTokens + 1][bl::kGqMaxWarps + 1] = {};    // and its CTAs per SM
-  bool gemv_split_attr_set[bl::kGemvMaxTokens + 1] = {};
-  int gemv_ep_blocks_per_sm[bl::kGemvEpMaxTokens + 1] = {};     // 0: not set up yet
-  bool gemv_ep_split_attr_set[bl::kGemvEpMaxTokens + 1] = {};
+  FlagFact gemm_attr_set[8] = {};
+  CountFact gemv_blocks_per_sm[bl::kGemvMaxTokens + 1] = {};   // 0: not set up yet
+  CountFact tl2_blocks_per_sm[bl::kGemvMaxTokens + 1] = {};    // 0: not set up yet
+  CountFact gq_max_dyn[bl::kGemvMaxTokens + 1] = {};   // dynamic shared memory limit
+  KeyedFact gq_occ[bl::kGemvMaxTokens + 1][bl::kGqMaxWarps + 1];   // CTAs per SM, by bytes
+  FlagFact gemv_split_attr_set[bl::kGemvMaxTokens + 1] = {};
+  CountFact gemv_ep_blocks_per_sm[bl::kGemvEpMaxTokens + 1] = {};  // 0: not set up yet
+  FlagFact gemv_ep_split_attr_set[bl::kGemvEpMaxTokens + 1] = {};
   NormKernelInfo norm[3][2][9];       // type, gated, width (launch_norm.cu)
-  bool split_attr_set[3] = {};        // gemm_split_kernel: 32, 64, 128 tokens
-  int split_clusters[3][3] = {};      // resident clusters of 1, 2, 4 pairs; 0: not asked yet
+  FlagFact split_attr_set[3] = {};    // gemm_split_kernel: 32, 64, 128 tokens
+  CountFact split_clusters[3][3] = {};   // resident clusters of 1, 2, 4 pairs; 0: not asked yet
 };
 
 // The calling thread's current device.

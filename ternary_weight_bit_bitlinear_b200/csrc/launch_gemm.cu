@@ -92,7 +92,7 @@ struct SplitLaunch {
 template <int BN>
 bitlinear_status split_config(int grid, int S, DeviceInfo* dev, cudaStream_t s, SplitLaunch& l) {
   const int smem = static_cast<int>(sizeof(bl::SplitSmem<BN>)) + 1024;
-  bool& set = dev->split_attr_set[split_width(BN)];
+  FlagFact& set = dev->split_attr_set[split_width(BN)];
   if (!set) {
     if (cudaFuncSetAttribute(bl::gemm_split_kernel<BN>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
@@ -142,16 +142,16 @@ bitlinear_status ask_clusters(int S, DeviceInfo* dev, int* out) {
 }  // namespace
 
 bitlinear_status split_clusters(int BN, int S, DeviceInfo* dev, int* out) {
-  int& known = dev->split_clusters[split_width(BN)][split_size(S)];
-  if (known == 0) {
-    int n = 0;
+  CountFact& known = dev->split_clusters[split_width(BN)][split_size(S)];
+  int n = known;
+  if (n == 0) {
     const bitlinear_status st = BN == 32   ? ask_clusters<32>(S, dev, &n)
                                 : BN == 64 ? ask_clusters<64>(S, dev, &n)
                                            : ask_clusters<128>(S, dev, &n);
     if (st != BITLINEAR_OK) return st;
     known = n;
   }
-  *out = known;
+  *out = n;
   return BITLINEAR_OK;
 }
 

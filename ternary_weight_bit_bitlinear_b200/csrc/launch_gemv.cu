@@ -7,12 +7,13 @@
 namespace blh {
 namespace {
 
-// per_sm, split_attr_set: this instantiation's once-per-device facts.
+// known (CTAs per SM), split_attr_set: this instantiation's once-per-device facts.
 template <int NT, class P>
-bitlinear_status launch_gemv_tile(const P& p, int& per_sm, bool& split_attr_set,
+bitlinear_status launch_gemv_tile(const P& p, CountFact& known, FlagFact& split_attr_set,
                                   DeviceInfo* dev, cudaStream_t s) {
   auto kernel = bl::gemv_tile_kernel<NT, P>;
   constexpr int smem = bl::GemvCfg<NT>::kSmemBytes;
+  int per_sm = known;
   if (per_sm == 0) {
     int nb = 0;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
@@ -21,7 +22,7 @@ bitlinear_status launch_gemv_tile(const P& p, int& per_sm, bool& split_attr_set,
             cudaSuccess ||
         nb < 1)
       return BITLINEAR_ERR_CUDA;
-    per_sm = nb;
+    known = per_sm = nb;
   }
   // Every warp resident at once, with the same number of units (give or take
   // one) per warp: units per warp first, then just enough warps.  A launch

@@ -10,7 +10,8 @@ namespace {
 template <int NT>
 bitlinear_status max_dyn_smem(DeviceInfo* dev, int* out) {
   auto kernel = bl::gemv_quant_kernel<NT>;
-  if (!dev->gq_attr_set[NT]) {
+  int dyn = dev->gq_max_dyn[NT];
+  if (dyn == 0) {
     int dev_id = 0, optin = 0;
     cudaFuncAttributes fa;
     if (cudaGetDevice(&dev_id) != cudaSuccess ||
@@ -18,15 +19,14 @@ bitlinear_status max_dyn_smem(DeviceInfo* dev, int* out) {
             cudaSuccess ||
         cudaFuncGetAttributes(&fa, kernel) != cudaSuccess)
       return BITLINEAR_ERR_CUDA;
-    const int dyn = optin - static_cast<int>(fa.sharedSizeBytes);
+    dyn = optin - static_cast<int>(fa.sharedSizeBytes);
     if (dyn <= 0 ||
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn) !=
             cudaSuccess)
       return BITLINEAR_ERR_CUDA;
     dev->gq_max_dyn[NT] = dyn;
-    dev->gq_attr_set[NT] = true;
   }
-  *out = dev->gq_max_dyn[NT];
+  *out = dyn;
   return BITLINEAR_OK;
 }
 
@@ -40,15 +40,14 @@ bitlinear_status occupancy_nt(int warps, int area, DeviceInfo* dev, int* out) {
     *out = 0;
     return BITLINEAR_OK;
   }
-  if (dev->gq_area[NT][warps] != area) {
-    int nb = 0;
+  int nb = 0;
+  if (!dev->gq_occ[NT][warps].get(area, &nb)) {
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&nb, kernel, 32 * warps, area) !=
         cudaSuccess)
       return BITLINEAR_ERR_CUDA;
-    dev->gq_area[NT][warps] = area;
-    dev->gq_occ[NT][warps] = nb;
+    dev->gq_occ[NT][warps].set(area, nb);
   }
-  *out = dev->gq_occ[NT][warps];
+  *out = nb;
   return BITLINEAR_OK;
 }
 

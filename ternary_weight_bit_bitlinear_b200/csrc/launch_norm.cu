@@ -22,14 +22,13 @@ bitlinear_status launch_stream(int rows, const bl::NormParams& p, NormKernelInfo
   }
   int grid = rows;
   if (rows > sms) {
-    int per_sm = known.per_sm;
-    if (per_sm == 0 || known.smem != smem) {
+    int per_sm = 0;
+    if (!known.per_sm.get(smem, &per_sm)) {
       if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, smem) !=
               cudaSuccess ||
           per_sm < 1)
         return BITLINEAR_ERR_CUDA;
-      known.smem = smem;
-      known.per_sm = per_sm;
+      known.per_sm.set(smem, per_sm);
     }
     if (grid > sms * per_sm) grid = sms * per_sm;
   }

@@ -9,7 +9,8 @@ template <int NT>
 bitlinear_status launch_gemv_tl2_nt(const bl::Tl2Params& p, DeviceInfo* dev, cudaStream_t s) {
   auto kernel = bl::gemv_tl2_kernel<NT>;
   constexpr int smem = bl::Tl2Cfg<NT>::kSmemBytes;
-  int& per_sm = dev->tl2_blocks_per_sm[NT];
+  CountFact& known = dev->tl2_blocks_per_sm[NT];
+  int per_sm = known;
   if (per_sm == 0) {
     int nb = 0;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
@@ -18,7 +19,7 @@ bitlinear_status launch_gemv_tl2_nt(const bl::Tl2Params& p, DeviceInfo* dev, cud
             cudaSuccess ||
         nb < 1)
       return BITLINEAR_ERR_CUDA;
-    per_sm = nb;
+    known = per_sm = nb;
   }
   const int64_t cap = static_cast<int64_t>(dev->sms) * per_sm * bl::kTl2Warps;
   const int64_t upw = (p.total_units + cap - 1) / cap;
