@@ -396,10 +396,12 @@ typedef struct {
  * Root-mean-square norm with the residual's addition, and int8 output with one
  * scale per token (the quantiser of bitlinear_quant_act behind it):
  *   h    = x, or with a residual x + residual rounded to dtype (written out)
- *   r    = 1 / sqrt(sum_k h^2 / K + eps)     in 64 bits, rounded once to fp32:
- *          it does not depend on the order of the sum, nor do the codes
+ *   r    = 1 / sqrt(sum_k h^2 / K + eps)     in 64 bits, rounded once to fp32
  *   v    = (h * r) * weight                   (v = h when normalize is 0)
  *   amax = max_k |v|;  xq, xsum as in bitlinear_quant_act
+ * The order of the sum is not part of the definition.  Two orders differ by a
+ * few 2^-53 of r, so r and the codes are the same in both unless the 64-bit
+ * value lies that near to the middle of two fp32 values: about one row in 10^8.
  * eps must be positive and finite, and weight NULL without the norm.  A row
  * whose v holds NaN or inf gets amax = NaN, xq = 0 and xsum = 0, so that its
  * products come out NaN; other rows are not affected.

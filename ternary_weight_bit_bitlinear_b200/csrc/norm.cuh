@@ -8,10 +8,12 @@
 //   v    = (h * r) * w                      without the norm, v = h
 //   amax = max |v|,  q = clamp(rint(v * (127 / amax)), -128, 127)
 //
-// The sum of squares and r are held in 64 bits and r is rounded once (squares
-// of fp32 values are exact there), so r, and with it every code, does not
-// depend on how the row is cut into threads: the result is the definition's,
-// as it is for the library's other integer results.  The maximum keeps inf and
+// The sum of squares and r are held in 64 bits and r is rounded once.  Squares
+// of fp32 values are exact there, their sum is not: how the row is cut into
+// threads changes it by a few 2^-53, and r, and the codes with it, only where
+// that reaches across the middle of two fp32 values (2^-24 apart from either:
+// about one row in 10^8).  Every other row comes out as the definition has it,
+// bit for bit.  The maximum keeps inf and
 // NaN: a row that holds either gets amax = NaN and q = 0.
 //
 // Two kernels, both reading each element once and holding it in registers from
