@@ -44,26 +44,6 @@ union Vec16 {
   T e[kVec<T>];
 };
 
-template <typename T>
-__device__ __forceinline__ void load_vec(const T* p, float (&f)[kVec<T>]) {
-  Vec16<T> v;
-  v.u = *reinterpret_cast<const uint4*>(p);
-#pragma unroll
-  for (int i = 0; i < kVec<T>; ++i) f[i] = Elem<T>::to_float(v.e[i]);
-}
-
-// Stores f rounded to T and leaves the rounded values in f.
-template <typename T>
-__device__ __forceinline__ void store_vec(T* p, float (&f)[kVec<T>]) {
-  Vec16<T> v;
-#pragma unroll
-  for (int i = 0; i < kVec<T>; ++i) {
-    v.e[i] = Elem<T>::from_float(f[i]);
-    f[i] = Elem<T>::to_float(v.e[i]);
-  }
-  *reinterpret_cast<uint4*>(p) = v.u;
-}
-
 // max(v, 0) that keeps a NaN.
 __device__ __forceinline__ float relu_nan(float v) {
   float r;

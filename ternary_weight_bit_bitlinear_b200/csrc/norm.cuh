@@ -13,8 +13,8 @@
 // threads changes it by a few 2^-53, and r, and the codes with it, only where
 // that reaches across the middle of two fp32 values (2^-24 apart from either:
 // about one row in 10^8).  Every other row comes out as the definition has it,
-// bit for bit.  The maximum keeps inf and
-// NaN: a row that holds either gets amax = NaN and q = 0.
+// bit for bit.  The maximum keeps inf and NaN: a row that holds either gets
+// amax = NaN and q = 0.
 //
 // Two kernels, both reading each element once and holding it in registers from
 // the load to the codes (kElems per thread, 8 to 48):
@@ -41,8 +41,6 @@
 #include "quant_math.cuh"
 
 namespace bl {
-
-constexpr int kNormRegElems = 32;   // the most values of a row that a thread keeps
 
 struct NormParams {
   const void* a;          // x, or gate
