@@ -477,6 +477,17 @@ BITLINEAR_API bitlinear_status bitlinear_linear(const bitlinear_linear_problem* 
                                                 int64_t count, int64_t N,
                                                 bitlinear_stream_t stream);
 
+/*
+ * How bitlinear_linear would run this call on the current device, for tests and
+ * measurements: *tokens is 0 for the CUDA cores, else the tokens of a
+ * tensor-core tile (32, 64, 128, or 256 for the kernel of long prompts), and
+ * *pairs the CTA pairs that share a tile's K (1, 2 or 4; 0 with *tokens 0).  A
+ * list that takes several launches: the first of them.  Launches nothing.
+ */
+BITLINEAR_API bitlinear_status bitlinear_linear_plan(const bitlinear_linear_problem* problems,
+                                                     int64_t count, int64_t N, int* tokens,
+                                                     int* pairs);
+
 /* ------------------------------------------------- weights, no allocation */
 
 /*

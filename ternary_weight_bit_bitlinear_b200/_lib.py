@@ -143,6 +143,9 @@ def load(path: str = LIB_PATH):
     L.bitlinear_gated_norm_quant.restype = st
     L.bitlinear_linear.argtypes = [ctypes.POINTER(LinearProblem), i64, i64, p]
     L.bitlinear_linear.restype = st
+    L.bitlinear_linear_plan.argtypes = [ctypes.POINTER(LinearProblem), i64, i64,
+                                        ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int)]
+    L.bitlinear_linear_plan.restype = st
     L.bitlinear_device_error.argtypes = [ctypes.POINTER(ctypes.c_int), ctypes.c_int]
     L.bitlinear_device_error.restype = st
     L.bitlinear_set_wait_limit.argtypes = [ctypes.c_ulonglong]
@@ -320,6 +323,14 @@ def bitlinear_gated_norm_quant(a, stream=None):
 def bitlinear_linear(problems, count, N, stream=None):
     """problems: a ctypes array of LinearProblem."""
     return load().bitlinear_linear(problems, count, N, _stream(stream))
+
+
+def bitlinear_linear_plan(problems, count, N):
+    """(tokens, pairs) of the call; problems: a ctypes array of LinearProblem."""
+    tokens, pairs = ctypes.c_int(), ctypes.c_int()
+    check(load().bitlinear_linear_plan(problems, count, N, ctypes.byref(tokens),
+                                       ctypes.byref(pairs)), "bitlinear_linear_plan")
+    return tokens.value, pairs.value
 
 
 def bitlinear_pack_workspace_bytes(M, K):

@@ -917,6 +917,28 @@ bitlinear_status bitlinear_linear(const bitlinear_linear_problem* problems, int6
   return linear_group(problems, count, N, reinterpret_cast<cudaStream_t>(stream));
 }
 
+bitlinear_status bitlinear_linear_plan(const bitlinear_linear_problem* problems, int64_t count,
+                                       int64_t N, int* tokens, int* pairs) {
+  if (count < 1 || N < 1 || !problems || !tokens || !pairs) return BITLINEAR_ERR_INVALID_ARG;
+  for (int64_t i = 0; i < count; ++i) {
+    const bitlinear_status st = check_linear_problem(problems[i], N);
+    if (st != BITLINEAR_OK) return st;
+  }
+  LinearPlan plan;
+  if (linear_on_cuda_cores(problems, count, N)) {
+    plan.BN = plan.S = 0;
+  } else {
+    DeviceInfo* dev = nullptr;
+    bitlinear_status st = device_info(&dev);
+    if (st != BITLINEAR_OK) return st;
+    const int n = static_cast<int>(std::min<int64_t>(count, bl::kGemmMaxProblems));
+    if ((st = plan_linear(problems, n, N, dev, &plan)) != BITLINEAR_OK) return st;
+  }
+  *tokens = plan.BN;
+  *pairs = plan.S;
+  return BITLINEAR_OK;
+}
+
 bitlinear_status bitlinear_norm_quant(const bitlinear_norm* a, bitlinear_stream_t stream) {
   if (!a) return BITLINEAR_ERR_INVALID_ARG;
   bitlinear_status st = check_norm(a->N, a->K, a->dtype, a->normalize, a->eps, a->weight, a->xq,
