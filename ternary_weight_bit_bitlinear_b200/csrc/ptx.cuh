@@ -85,22 +85,21 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
 
 // Wait for the phase with the given parity to complete.  Gives up (returns
 // false, sets *abort and the device error word) after limit_ns, or as soon as
-// another role of the same CTA has given up (*abort != 0).
+// another role of the same CTA has given up (*abort != 0).  A try suspends the
+// thread for a few us, so both are looked at after every try.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
                                           unsigned long long limit_ns) {
   if (mbar_try_wait(bar, parity)) return true;
-  unsigned long long t0 = global_timer_ns();
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 7u) == 0) {
-      if (*abort) return false;
-      if (global_timer_ns() - t0 > limit_ns) {
-        *abort = 1;
-        atomicOr(&g_device_error, kDeviceTimeout);
-        return false;
-      }
+  const unsigned long long t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort) return false;
+    if (global_timer_ns() - t0 > limit_ns) {
+      *abort = 1;
+      atomicOr(&g_device_error, kDeviceTimeout);
+      return false;
     }
   }
+  return true;
 }
 
 // mbar_wait by every lane of a warp, with one answer for all of them: when
@@ -455,18 +454,16 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
                                                   volatile int* abort,
                                                   unsigned long long limit_ns) {
   if (mbar_try_wait_cluster(bar, parity)) return true;
-  unsigned long long t0 = global_timer_ns();
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    if ((i & 7u) == 0) {
-      if (*abort) return false;
-      if (global_timer_ns() - t0 > limit_ns) {
-        *abort = 1;
-        atomicOr(&g_device_error, kDeviceTimeout);
-        return false;
-      }
+  const unsigned long long t0 = global_timer_ns();
+  while (!mbar_try_wait_cluster(bar, parity)) {
+    if (*abort) return false;
+    if (global_timer_ns() - t0 > limit_ns) {
+      *abort = 1;
+      atomicOr(&g_device_error, kDeviceTimeout);
+      return false;
     }
   }
+  return true;
 }
 
 // mbar_wait_cluster by every lane of a warp, one answer for all lanes (see

@@ -4,8 +4,8 @@ takes is asked for, so that a case reaches what it is here for.
 The CTA-pair kernel of long prompts (256 tokens a tile) is taken where there are
 many row blocks and more than 128 tokens; its epilogue is run here with ragged
 rows, odd strides, in place, all types and activations, and lists whose layers
-differ.  The way out of a wait that ran out is run too, with one and
-two pairs per tile.
+differ.  The way out of a wait that ran out is run too, with one, two
+and four pairs per tile.
 """
 import numpy as np
 import pytest
@@ -189,12 +189,14 @@ def test_pair_kernel_far_arguments(dtype, name):
 
 # --------------------------------------------------- waits that run out
 
-# The limit is 2 us.  A tile's accumulators take 1024 k-blocks, 100 us, or half of
-# that; 40 k-blocks, 13 us, in the pair kernel, which long K does not choose.
+# The limit is 2 us; a try of a wait takes a few, and the clock is looked at after
+# each.  A tile's accumulators take 1024 k-blocks, 100 us, or that over the pairs;
+# 40 k-blocks, 13 us, in the pair kernel, which long K does not choose.
 LONG = 131072
 WAITS = [(32, 1, 16, 256 * 74, LONG), (64, 1, 64, 256 * 74, LONG), (128, 1, 128, 256 * 74, LONG),
          (32, 2, 3, 256 * 20, LONG), (64, 2, 64, 256 * 20, LONG), (128, 2, 100, 256 * 20, LONG),
-         (256, 1, 1024, 256 * 74, 5120)]
+         (32, 4, 3, 200, LONG), (32, 4, 9, 256 * 11, LONG), (64, 4, 64, 256 * 11, LONG),
+         (128, 4, 100, 256 * 11, LONG), (256, 1, 1024, 256 * 74, 5120)]
 
 
 @pytest.mark.parametrize("tokens,pairs,N,M,K", WAITS)
