@@ -382,7 +382,11 @@ bitlinear_status linear_split(const bitlinear_linear_problem* probs, int n, int6
 //   2560 x 2560, 128 tokens:  9.3 / 9.0 / 8.2 for S = 1 / 2 / 4
 //   8192 x 28672, 16 tokens: 28.4 / 18.7 / 24.3;  128 tokens: 43.4 / 27.8 / 37.0
 //   11008 x 4096, 16 tokens:  8.3 / 10.0 / 11.8 (43 tiles fit in no two rounds)
-//   11008 x 4096, 512 tokens: 30.0 at BN = 128, 33.9 at 256; 2048: 94.8 and 72.3
+//   11008 x 4096, 512 tokens: 29.9 at BN = 64 (taken: 24.2 without the launch),
+//   30.0 at 128, 33.9 at 256; 2048: 94.8 at 128 and 72.3 at 256 (taken)
+// The epilogue is priced alike whatever it does; rows that are not on 16 bytes
+// and an fp32 silu cost more (93 x 11005 x 4112: 10.9 estimated, 14.2 measured
+// without an activation, 16.6 with silu).
 struct LinearPlan {
   int BN = 0, S = 1;
   int64_t cost = INT64_MAX;

@@ -75,9 +75,9 @@ bitlinear_status launch_cluster(int64_t rows, int C, bl::NormParams p, cudaStrea
 // threads 14.6 / 17.7 / 29.7 us), with few registers a thread past the row's
 // end (their zeros run through all of the arithmetic: 2048 x 2560 bf16 in
 // 160 threads of 16 values 10.2 us, in 128 of 32 12.2; 512 rows 4.7 and 5.6).
-// Up to 12288 elements of 16 bits, where instructions bound it, two CTAs of 256
-// threads with 48 values each go through their reductions in turn, against one
-// of 512 with 24 (gate and up 512 x 11008: 11.3 and 13.5 us, 2048: 30.6 and
+// Up to 12288 elements of 16 bits two CTAs of 256 threads with 48 values each
+// take turns at the steps that wait, against one of 512 with 24, whose SM waits
+// with it (gate and up 512 x 11008: 11.3 and 13.5 us, 2048: 30.6 and
 // 39.8); one row for an SM (64: 7.5 and 5.9) and fp32 (2048: 51.5 and 49.0)
 // take the wide one.  The same trade at other widths: no gain at 2048 rows of
 // 5120 to 8192, 1.1 times the time at 14336 and 16384 (64 values).

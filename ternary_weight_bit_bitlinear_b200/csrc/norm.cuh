@@ -29,10 +29,12 @@
 // The waits are bounded, as everywhere.
 //
 // Bound by memory in fp32 with a residual (2048 x 8192: 37.6 us, 5.8 TB/s of
-// the 13 bytes an element), by instructions where the elements are 16 bits
-// wide (2048 x 4096 bf16 with a residual: 13.2 us, 4.4 TB/s; gate and up
-// 2048 x 6912: 22.9 us, 3.1 TB/s): some 20 per element, the conversion to 64
-// bits among them (16 a cycle and SM).  One token: 2.5 us at 2560, 3.2 at
+// the 13 bytes an element).  Rows of 16 bits are bound by the latency of one
+// step after another with few warps per SM (2048 x 4096 bf16 with a residual:
+// 13.3 us, 4.4 TB/s, 19 warps; gate and up 2048 x 6912: 22.9 us, 3.1 TB/s, 16):
+// their 26 and 30 instructions an element fill half of the issue slots, no pipe
+// is above 41 % (ALU) and DRAM is at 25 % of its peak; a warp waits for shared
+// memory and shuffles, for the next row's copy and for barriers.  One token: 2.5 us at 2560, 3.2 at
 // 8192 (launch to launch), 4.0 at 28672, where one CTA would take 14.6.
 #pragma once
 
