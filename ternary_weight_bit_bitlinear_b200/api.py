@@ -54,17 +54,29 @@ def _launch(fn, name, dev, stream, *args):
         raise _lib.BitLinearError(status, name)
 
 
+def _handle(stream):
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _as_stream(stream, device):
+    """torch's object for a stream, or for the handle of one.  (0 is the default
+    stream's; ExternalStream takes it for no handle and makes a new stream.)"""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = _handle(stream)
+    if handle == 0:
+        return torch.cuda.default_stream(device)
+    return torch.cuda.ExternalStream(handle, device=device)
+
+
 def _allocate(stream, like, *shapes):
     """Uninitialised tensors beside `like`, (shape, dtype) each, that belong to
     the stream that will write them: nothing pending elsewhere still uses their
     memory, and once dropped it is not handed out again before that stream is
     done with it.  Outputs, codes and workspaces all come from here."""
-    if stream is None:
+    if stream is None or _handle(stream) == _lib.raw_stream(None, like.device.index):
         return [like.new_empty(s, dtype=d) for s, d in shapes]
-    if not isinstance(stream, torch.cuda.Stream):
-        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        stream = torch.cuda.ExternalStream(handle, device=like.device)
-    with torch.cuda.stream(stream):
+    with torch.cuda.stream(_as_stream(stream, like.device)):
         return [like.new_empty(s, dtype=d) for s, d in shapes]
 
 
@@ -620,6 +632,13 @@ class TernaryLinear:
                       out_dtype, out, stream)
 
     def __call__(self, x, stream=None):
+        dev = self.packed.device
+        if stream is None or _handle(stream) == _lib.raw_stream(None, dev.index):
+            return self._apply(x, stream)
+        with torch.cuda.stream(_as_stream(stream, dev)):   # once for all that is allocated
+            return self._apply(x, stream)
+
+    def _apply(self, x, stream):
         if self.bias is not None:
             return self.quantized(*quant_act(x, stream), stream=stream)
         if use_fused_decode(x.shape[0], x.shape[1]):

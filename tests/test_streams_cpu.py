@@ -15,6 +15,7 @@ import torch
 from ternary_weight_bit_bitlinear_b200 import _lib, api, build
 
 DEV = torch.device("cpu")
+CURRENT = 0x11          # the handle of the current stream
 
 
 class Stream:
@@ -48,10 +49,18 @@ def record(monkeypatch):
     _lib.load()
     r = Record()
 
-    def external(handle, device=None):
+    def of(h):
         s = Stream()
-        s.cuda_stream = handle
+        s.cuda_stream = h
         return s
+
+    def external(h, device=None):          # torch takes 0 for "none given": a new stream
+        return of(h or 0xE0)
+
+    def handle(s):                         # that a call given `s` launches on
+        if s is None:
+            return r.streams[-1] if r.streams else CURRENT
+        return getattr(s, "cuda_stream", s)
 
     def noting(fn):
         def f(*a, **kw):
@@ -61,13 +70,14 @@ def record(monkeypatch):
 
     def entry(name):
         def f(*a):
-            r.called.append((name, r.devices[-1] if r.devices else None))
+            r.called.append((name, r.devices[-1] if r.devices else None, handle(a[-1])))
             return _lib.OK
         return f
 
     monkeypatch.setattr(api, "_need", lambda *a: None)
     monkeypatch.setattr(torch.cuda, "Stream", Stream)
     monkeypatch.setattr(torch.cuda, "ExternalStream", external)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: of(0))
     monkeypatch.setattr(torch.cuda, "stream", r.stream)
     monkeypatch.setattr(torch.cuda, "device", r.device)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)   # never the tensors' own
@@ -84,7 +94,7 @@ def record(monkeypatch):
         def __getattr__(self, name):
             return getattr(lib, name)
     monkeypatch.setattr(_lib, "load", lambda *a: Calls())
-    monkeypatch.setattr(_lib, "raw_stream", lambda s, i: getattr(s, "cuda_stream", s) or 0)
+    monkeypatch.setattr(_lib, "raw_stream", lambda s, i: handle(s))
     return r
 
 
@@ -127,19 +137,23 @@ CALLS = {
 def test_memory_of_a_call_belongs_to_its_stream(record, name):
     class Other:                                        # another library's stream
         cuda_stream = 0x99
-    for given in (Stream(), 0x77, Other()):             # 0x77: a raw handle
+    for given in (Stream(), 0x77, 0, Other()):          # raw handles; 0: the default stream
         record.allocated.clear()
         record.called.clear()
         CALLS[name](given)
         want = getattr(given, "cuda_stream", given)
         assert record.called and record.allocated
         assert all(s == want for s in record.allocated), (record.allocated, want)
+        assert all(s == want for _, _, s in record.called), (record.called, want)
 
 
 @pytest.mark.parametrize("name", sorted(CALLS))
 def test_without_a_stream_nothing_changes_the_current_one(record, name):
-    CALLS[name](None)
-    assert record.called and record.allocated and set(record.allocated) == {None}
+    for given in (None, CURRENT):
+        record.allocated.clear()
+        CALLS[name](given)
+        assert record.called and record.allocated and set(record.allocated) == {None}
+        assert {s for _, _, s in record.called} == {CURRENT}
 
 
 @pytest.mark.parametrize("name", sorted(CALLS))
@@ -147,4 +161,4 @@ def test_calls_launch_with_the_device_of_their_tensors_current(record, name):
     """Another device may be current: the pointers are of the tensors' own."""
     for given in (None, Stream()):
         CALLS[name](given)
-    assert record.called and all(d == DEV for _, d in record.called), record.called
+    assert record.called and all(d == DEV for _, d, _ in record.called), record.called

@@ -72,3 +72,23 @@ def test_packing_on_a_busy_stream():
     assert torch.equal(p, packed) and torch.equal(a, alpha)
     assert all(map(torch.equal, got, want))
     assert all((t == 7).all() for t in marks)
+
+
+def test_handle_of_the_default_stream():
+    """0 is a stream like another: a call given it from within another stream
+    allocates and runs there."""
+    x = inputs.activations(6, K, seed=6, device="cuda")
+    W = inputs.latent_weights(M, K, seed=7, device="cuda")
+    layer = api.TernaryLinear.from_float(W, bias=torch.randn(M, device="cuda"))
+    want, codes = layer(x), api.norm_quant(x)
+    default, s = torch.cuda.default_stream(), torch.cuda.Stream()
+    assert default.cuda_stream == 0
+    torch.cuda.synchronize()
+    for given in (0, default):
+        torch.cuda._sleep(SLEEP)
+        with torch.cuda.stream(s):
+            got, again = layer(x, stream=given), api.norm_quant(x, stream=given)
+            marks = same_sizes(6)                        # on s, which runs on
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and all(map(torch.equal, again, codes))
+        assert all((t == 7).all() for t in marks)
