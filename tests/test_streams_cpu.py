@@ -27,14 +27,19 @@ class Record:
     at each call of an entry point."""
 
     def __init__(self):
-        self.streams, self.devices = [], []
-        self.allocated, self.called = [], []
+        self.streams, self.devices = [CURRENT], []
+        self.allocated, self.called, self.set_devices = [], [], []
 
-    @contextlib.contextmanager
-    def stream(self, s):
-        self.streams.append(s.cuda_stream)
-        yield
-        self.streams.pop()
+    def current(self, device=None):
+        s = Stream()
+        s.cuda_stream = self.streams[-1]
+        return s
+
+    def set(self, s):      # back to the one before, or on to another
+        if len(self.streams) > 1 and self.streams[-2] == s.cuda_stream:
+            self.streams.pop()
+        else:
+            self.streams.append(s.cuda_stream)
 
     @contextlib.contextmanager
     def device(self, d):
@@ -59,12 +64,12 @@ def record(monkeypatch):
 
     def handle(s):                         # that a call given `s` launches on
         if s is None:
-            return r.streams[-1] if r.streams else CURRENT
+            return r.streams[-1]
         return getattr(s, "cuda_stream", s)
 
     def noting(fn):
         def f(*a, **kw):
-            r.allocated.append(r.streams[-1] if r.streams else None)
+            r.allocated.append(r.streams[-1])
             return fn(*a, **kw)
         return f
 
@@ -78,7 +83,9 @@ def record(monkeypatch):
     monkeypatch.setattr(torch.cuda, "Stream", Stream)
     monkeypatch.setattr(torch.cuda, "ExternalStream", external)
     monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: of(0))
-    monkeypatch.setattr(torch.cuda, "stream", r.stream)
+    monkeypatch.setattr(torch.cuda, "current_stream", r.current)
+    monkeypatch.setattr(torch.cuda, "set_stream", r.set)
+    monkeypatch.setattr(torch.cuda, "set_device", lambda d: r.set_devices.append(d))
     monkeypatch.setattr(torch.cuda, "device", r.device)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)   # never the tensors' own
     monkeypatch.setattr(torch, "empty", noting(torch.empty))
@@ -145,6 +152,8 @@ def test_memory_of_a_call_belongs_to_its_stream(record, name):
         assert record.called and record.allocated
         assert all(s == want for s in record.allocated), (record.allocated, want)
         assert all(s == want for _, _, s in record.called), (record.called, want)
+        assert record.streams == [CURRENT]              # as it was before the call
+        assert set(record.set_devices) == {-1}          # and the device
 
 
 @pytest.mark.parametrize("name", sorted(CALLS))
@@ -152,7 +161,7 @@ def test_without_a_stream_nothing_changes_the_current_one(record, name):
     for given in (None, CURRENT):
         record.allocated.clear()
         CALLS[name](given)
-        assert record.called and record.allocated and set(record.allocated) == {None}
+        assert record.called and record.allocated and set(record.allocated) == {CURRENT}
         assert {s for _, _, s in record.called} == {CURRENT}
 
 
