@@ -62,6 +62,8 @@ def _as_stream(stream, device):
     """torch's object for a stream, or for the handle of one.  (0 is the default
     stream's; ExternalStream takes it for no handle and makes a new stream.)"""
     if isinstance(stream, torch.cuda.Stream):
+        if stream.device != device:
+            raise ValueError("the stream is of %s, the tensors are on %s" % (stream.device, device))
         return stream
     handle = _handle(stream)
     if handle == 0:

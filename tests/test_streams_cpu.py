@@ -20,6 +20,7 @@ CURRENT = 0x11          # the handle of the current stream
 
 class Stream:
     cuda_stream = 0x51
+    device = DEV
 
 
 class Record:
@@ -171,3 +172,12 @@ def test_calls_launch_with_the_device_of_their_tensors_current(record, name):
     for given in (None, Stream()):
         CALLS[name](given)
     assert record.called and all(d == DEV for _, d, _ in record.called), record.called
+
+
+@pytest.mark.parametrize("name", sorted(CALLS))
+def test_a_stream_of_another_device_is_refused(record, name):
+    given = Stream()
+    given.device = torch.device("cuda", 1)
+    with pytest.raises(ValueError, match="stream"):
+        CALLS[name](given)
+    assert not record.called and record.streams == [CURRENT]
